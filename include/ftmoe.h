@@ -535,6 +535,85 @@ FT_API int ft_expert_ffn_decode_noalloc(const void* x, int T, int H, int I, int 
                                         const float* gates, const int* inv, int has_shared, void* out,
                                         void* stream);
 
+/* ------------------------------------------------------------------------ *
+ * 8-bit floating point around the layer (step level).  The pages name no such format; it
+ * is the e4m3 release format of current MoE checkpoints: weights as e4m3 codes with an f32
+ * scale per block of 128 rows x 128 columns, activation rows as e4m3 codes with an f32
+ * scale per 128 consecutive columns.  A value is code * scale.  A width that is not a
+ * multiple of 128 ends in a partial block with a scale of its own.
+ *
+ * A transformer block on such a checkpoint calls, around the routing above:
+ *   ft_rmsnorm_fp8     residual + norm: y for ft_router_topk / ft_route_decode, and e4m3 rows
+ *   ft_expert_ffn_fp8  the selected (and shared) experts on those rows, then ft_combine
+ *   ft_quantize_fp8, ft_gemm_fp8   an attention output and its projection, or any dense layer
+ *
+ * All four allocate nothing, launch on `stream`, return after the launch and keep nothing
+ * between calls, so they may be captured into a graph and run on several streams at once
+ * (each on its own outputs and scratch).  All pointers but the host lists are device memory of the
+ * current device; the output is checked (FT_ERR_INVALID).  Every refusal leaves a message
+ * in ft_last_error(NULL).  Sizes of 0 tokens, rows or columns are calls that do nothing.
+ * ------------------------------------------------------------------------ */
+
+/* Residual addition, root-mean-square norm and e4m3 rows in one pass:
+ *   r = x + residual, rounded to x's type (the stored stream; r = x without residual)
+ *   y = r / sqrt(mean over H of r^2 + eps) * weight                   (f32)
+ *   s = max(max |y| / 448, 2^-126) per 128 columns;  q = e4m3(y * (1 / s))
+ * q is rounded to nearest even from the f32 y.  A NaN or infinity in y makes its block's
+ * scale NaN or infinite (so every value of the block is NaN) and leaves the other rows alone.
+ *   x: [T][H], rows ldx elements apart, bf16 if x_is_bf16 else f32; residual (may be NULL) and
+ *   residual_out (may be NULL; receives r): [T][H], rows ldr apart, x's type; residual_out may
+ *   be residual, or x when ldx == ldr.  weight: [H], x's type.  y (may be NULL): [T][H] contiguous, x's type.
+ *   q (may be NULL, y not both): bytes, rows ldq apart; the bytes past H of a row are not
+ *   written.  scales: [T][ceil(H / 128)] f32.  1 <= H <= 32768, any strides of at least H.
+ *   eps >= 0.  Rows whose widths, strides and addresses allow 16-byte accesses (H, the strides
+ *   multiples of 8) run faster. */
+FT_API int ft_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* weight,
+                          int x_is_bf16, int T, int H, float eps, void* residual_out, void* y, void* q, long long ldq,
+                          float* scales, void* stream);
+
+/* The e4m3 rows and scales of ft_rmsnorm_fp8 with y = x (no norm, no weight). */
+FT_API int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, int H, void* q, long long ldq,
+                           float* scales, void* stream);
+
+/* out = A W^T on e4m3 operands:
+ *   out[m][n] = sum over blocks b of K of a_scales[m][b] * w_scales[n / 128][b] *
+ *               (sum over k in b of a[m][k] * w[n][k])
+ * Tensor cores inside a block of 128, f32 sums across blocks.  The product of two scales that
+ * meet has to be a finite f32.
+ *   a: [M][K] e4m3, rows lda bytes apart; a_scales: [M][ceil(K / 128)] f32 (as ft_rmsnorm_fp8 and
+ *   ft_quantize_fp8 write them).  w: [N][K] e4m3, rows ldw bytes apart; w_scales:
+ *   [ceil(N / 128)][ceil(K / 128)] f32.  out: [M][N], rows ldo elements apart, bf16 (round to
+ *   nearest even) if out_is_bf16 else f32.  Any M, N and K >= 1; lda and ldw multiples of 16,
+ *   a and w 16-byte aligned; bytes past K of a row are not read as values.
+ *   err: a DEVICE int, 0 before the call; a kernel whose bounded pipeline wait gives up writes
+ *   121-124 there (the outputs are then incomplete). */
+FT_API int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
+                       const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
+                       void* stream);
+
+/* Bytes of one fp8 expert: W_gate [I][H], W_up [I][H], W_down [H][I] e4m3 codes, then their f32
+ * scales S_gate and S_up [ceil(I/128)][ceil(H/128)], S_down [ceil(H/128)][ceil(I/128)], padded
+ * to a multiple of 16.  0 unless H and I are positive multiples of 16. */
+FT_API size_t ft_fp8_blob_bytes(int H, int I);
+
+/* SwiGLU FFN of a list of experts on e4m3 weights and rows, from one token to long prefills:
+ *     h[q] = silu(W_gate x_t) * (W_up x_t), quantised like every activation row
+ *     y[q] = W_down h[q]                                                  (f32)
+ * for the pairs q of every entry, as in ft_expert_ffn_prefill: routed expert experts[i] owns q in
+ * [offsets[e], offsets[e+1]) with token t = perm[q] / top_k, experts[i] = -1 (the shared expert)
+ * q = T*top_k + t for every token t.  An expert is listed at most once.
+ *   x: [T][H] e4m3, rows ldx bytes apart (a multiple of 16, 16-byte aligned); x_scales:
+ *   [T][ceil(H / 128)].  weights: n_slots blobs (ft_fp8_blob_bytes apart, 16-byte aligned);
+ *   entry i's weights are blob slots[i].  experts, slots: HOST arrays of n_list entries
+ *   (n_list <= FT_MAX_EXPERTS + 1).  offsets [E+1], perm [T*top_k]: as written by ft_permute.
+ *   h: [T*top_k + T][I] bytes and h_scales: [T*top_k + T][ceil(I / 128)] f32, written: the
+ *   quantised rows between the two products.  y: [T*top_k + T][H] f32, written.  Rows that no entry owns are
+ *   left as they are.  H and I: multiples of 16.  T * (top_k + 1) < 2^31.  err: as in ft_gemm_fp8. */
+FT_API int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
+                             const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
+                             const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
+                             void* stream);
+
 /* Version string of the library build. */
 FT_API const char* ft_version(void);
 

@@ -65,6 +65,7 @@ class ft_access_t(ctypes.Structure):
 
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _SIGS = {
     "ft_moe_create": ([_i, _i, _i, _i, _i, _i], _vp),
     "ft_moe_set_layers": ([_vp, _i, _i, _i], _i),
@@ -95,6 +96,12 @@ _SIGS = {
                               _i),
     "ft_expert_ffn_decode_noalloc": ([_vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i,
                                       _vp, _vp], _i),
+    "ft_rmsnorm_fp8": ([_vp, _ll, _vp, _ll, _vp, _i, _i, _i, _f, _vp, _vp, _vp, _ll, _vp, _vp], _i),
+    "ft_quantize_fp8": ([_vp, _ll, _i, _i, _i, _vp, _ll, _vp, _vp], _i),
+    "ft_gemm_fp8": ([_vp, _ll, _vp, _vp, _ll, _vp, _i, _i, _i, _i, _vp, _ll, _vp, _vp], _i),
+    "ft_fp8_blob_bytes": ([_i, _i], _sz),
+    "ft_expert_ffn_fp8": ([_vp, _ll, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+                          _i),
     "ft_version": ([], ctypes.c_char_p),
     "ft_moe_set_stage_timing": ([_vp, _i], _i),
     "ft_moe_sync": ([_vp], _i),
@@ -342,6 +349,36 @@ def ft_expert_ffn_prefill(x, T, H, I, top_k, weights, n_slots, experts, slots, o
 def ft_combine(y, gates, inv, T, H, top_k, has_shared, out_is_bf16, out, stream=None):
     return _check(None, _lib.ft_combine(_p(y), _p(gates), _p(inv), T, H, top_k, int(has_shared),
                                         int(out_is_bf16), _p(out), _s(stream)))
+
+
+def ft_rmsnorm_fp8(x, ldx, residual, ldr, weight, x_is_bf16, T, H, eps, residual_out, y, q, ldq, scales, stream=None):
+    return _check(None, _lib.ft_rmsnorm_fp8(_p(x), ldx, _p(residual), ldr, _p(weight), int(x_is_bf16), T, H, eps,
+                                            _p(residual_out), _p(y), _p(q), ldq, _p(scales), _s(stream)))
+
+
+def ft_quantize_fp8(x, ldx, x_is_bf16, T, H, q, ldq, scales, stream=None):
+    return _check(None, _lib.ft_quantize_fp8(_p(x), ldx, int(x_is_bf16), T, H, _p(q), ldq, _p(scales), _s(stream)))
+
+
+def ft_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, stream=None):
+    return _check(None, _lib.ft_gemm_fp8(_p(a), lda, _p(a_scales), _p(w), ldw, _p(w_scales), M, N, K, int(out_is_bf16),
+                                         _p(out), ldo, _p(err), _s(stream)))
+
+
+def ft_fp8_blob_bytes(H, I):
+    return _lib.ft_fp8_blob_bytes(H, I)
+
+
+def ft_expert_ffn_fp8(x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets, perm, h, h_scales, y,
+                      err, stream=None):
+    if len(experts) != len(slots):
+        raise ValueError("experts and slots must have the same length")
+    n = len(experts)
+    ex = _int_array(experts or [0])
+    sl = _int_array(slots or [0])
+    return _check(None, _lib.ft_expert_ffn_fp8(
+        _p(x), ldx, _p(x_scales), T, H, I, top_k, _p(weights), n_slots, ctypes.cast(ex, ctypes.c_void_p),
+        ctypes.cast(sl, ctypes.c_void_p), n, _p(offsets), _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _s(stream)))
 
 
 def ft_cache_simulate(num_layers, num_experts, capacity, ops):

@@ -1,0 +1,32 @@
+// Device helpers of the fp8 kernels.
+#pragma once
+#include "common.cuh"
+
+namespace ftk {
+
+// Largest magnitude of a block, a NaN winning over every number (fmaxf would drop it).
+FT_DEVICE float amax_nan(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+// Scale of a block with largest magnitude amax: 448 is the largest e4m3 value; the floor
+// 2^-126 keeps the inverse finite for a block of zeros.  A NaN stays one.
+FT_DEVICE float fp8_scale(float amax) {
+  const float s = amax / 448.0f;
+  return s < 1.17549435e-38f ? 1.17549435e-38f : s;
+}
+// Two fp32 values -> two e4m3 codes (lo in the low byte): round to nearest even, saturating at +-448.
+FT_DEVICE uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two fp32 values -> a bf16 pair (lo in the low half), round to nearest even, NaN kept.
+FT_DEVICE uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace ftk

@@ -1,0 +1,356 @@
+// Block-scaled fp8 products for many rows on the 5th-generation tensor cores
+// (tcgen05 + TMEM, TMA), dense or grouped by expert:
+//
+//   out[m][n] = sum_kb sa[m][kb] sw[n / 128][kb] (sum_{k in block kb} a[m][k] w[n][k])
+//
+// mode 0 (gate/up): two such products over the same rows, h = silu(gate) * up, and h
+// quantised like every activation row: hs = max(max |h| / 448, 2^-126) per 128 columns,
+// code = e4m3(h * (1 / hs)).  mode 1: the product, stored as f32 or bf16.
+//
+// The scales differ from block to block of K, so the tensor cores may only sum inside one
+// block: every 128 of K the accumulators leave TMEM and are added, scaled, to fp32 sums in
+// registers.  A thread owns one row, so the factor sa * sw is one number for all its columns.
+//
+// One persistent kernel, one CTA per SM, 128 x 256 tiles:
+//   warp 0     TMA producer: per 128 of K, A 128 rows (gate/up: the pairs' token rows, gathered
+//              four at a time) and 256 weight rows, 128-byte swizzle, 4 stages of 48 KB.
+//   warp 1     MMA issuer: tcgen05.mma kind::f8f6f4, M=128, N=256, K=32, into two TMEM buffers
+//              of 256 columns in turn, so the tensor cores fill one while the other is read.
+//   warps 2-9  sums: warp w reads TMEM lanes 32 (w % 4).. of one half of the columns, adds
+//              them to 128 sums per thread, and at the end of a tile stores them.
+// gate/up tiles hold 128 gate and 128 up columns; each half of the warps takes 64 columns of
+// both, so silu(gate) * up stays inside a thread.
+//
+// Every wait is bounded: a thread that gives up records 121-124 in *err and raises the CTA's
+// abort flag; all roles then leave and TMEM is released.
+#include "fp8.hpp"
+#include "fp8_common.cuh"
+#include "fp8_mma.cuh"
+
+namespace ftk {
+namespace {
+
+constexpr int BM = 128, BN = 256, BK = kFp8Block;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 4, TMEM_COLS = 512;
+constexpr int SUM_WARPS = 8, THREADS = 64 + 32 * SUM_WARPS;
+
+struct Smem {
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], halves;
+  uint32_t tmem_base;
+  int abort;
+  int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
+  int row_start[kMaxList];
+  int rows[kMaxList];
+  float amax[2][2][BM];         // gate/up: a row's largest |h| per half, double-buffered by tile
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1)
+fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ GemmGroups groups,
+                const __grid_constant__ Fp8Gemm p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Smem* S = reinterpret_cast<Smem*>(base + STAGES * STAGE_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (p.K + BK - 1) / BK;
+  constexpr int TN = MODE == 0 ? BN / 2 : BN;   // output columns of a tile
+  const int n_tiles = (p.N + TN - 1) / TN;
+  int* err = p.err;
+
+  for (int g = threadIdx.x; g < groups.n; g += THREADS) {
+    const int e = groups.expert[g];
+    const int r0 = e >= 0 ? p.offsets[e] : p.T * p.k;
+    S->row_start[g] = r0;
+    S->rows[g] = e >= 0 ? p.offsets[e + 1] - r0 : p.T;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&S->full[s], 1);
+      mbar_init(&S->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&S->tfull[b], 1);
+      mbar_init(&S->tempty[b], 32 * SUM_WARPS);
+    }
+    mbar_init(&S->halves, 32 * SUM_WARPS);
+    S->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&S->tmem_base)), "r"(TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  __syncthreads();
+  if (warp == 0) {   // prefix sum of the groups' M-tiles
+    int acc = 0;
+    for (int g0 = 0; g0 < groups.n; g0 += 32) {
+      const int g = g0 + lane;
+      int v = g < groups.n ? (S->rows[g] + BM - 1) / BM : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (g < groups.n) S->mt_start[g + 1] = acc + v;
+      acc += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (lane == 0) S->mt_start[0] = 0;
+  }
+  fp8_fence_before();
+  __syncthreads();
+  fp8_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  const long long total_tiles = (long long)S->mt_start[groups.n] * n_tiles;
+  volatile int* abort_flag = &S->abort;
+
+  // tile -> (group, m-tile, n-tile): the M-tiles that share a weight tile run back to back
+  auto decode = [&](long long t, int& g, int& m, int& n) {
+    int lo = 0, hi = groups.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)S->mt_start[mid] * n_tiles <= t) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    const long long local = t - (long long)S->mt_start[g] * n_tiles;
+    const int mtg = S->mt_start[g + 1] - S->mt_start[g];
+    n = (int)(local / mtg);
+    m = (int)(local - (long long)n * mtg);
+  };
+
+  if (warp == 0) {   // ------------------------------------------------ TMA producer
+    int it = 0;
+    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+      int g, m, n;
+      decode(t, g, m, n);
+      const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
+      int tok[4];
+      if (MODE == 0) {   // lane l gathers tile rows 4l .. 4l+3; rows past the group repeat its last
+        const int last = S->row_start[g] + S->rows[g] - 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = min(row0 + 4 * lane + i, last);
+          tok[i] = groups.expert[g] < 0 ? q - p.T * p.k : p.perm[q] / p.k;
+        }
+      }
+      bool stop = false;
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int s = it % STAGES;
+        bool ok = true;
+        unsigned char* sa = base + s * STAGE_BYTES;
+        unsigned char* sb = sa + A_BYTES;
+        if (lane == 0) {
+          ok = mbar_wait(&S->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121);
+          if (ok) {
+            mbar_expect_tx(&S->full[s], STAGE_BYTES);
+            if (MODE == 1) fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
+            fp8_tma_3d(sb, &maps.b[0], &S->full[s], kb * BK, n * TN, z);
+            fp8_tma_3d(sb + B_BYTES / 2, &maps.b[1], &S->full[s], kb * BK, MODE == 0 ? n * TN : n * TN + BN / 2, z);
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) { stop = true; break; }
+        if (MODE == 0)
+          fp8_tma_gather4(sa + lane * 4 * BK, &maps.a, &S->full[s], kb * BK, tok[0], tok[1], tok[2], tok[3]);
+      }
+      if (stop) break;
+    }
+    // drain: wait (bounded) until every issued stage has landed
+    for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
+  } else if (warp == 1) {
+    if (lane == 0) {   // ---------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = fp8_idesc(BM, BN);
+      int it = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % STAGES, b = it & 1;
+          ok = mbar_wait(&S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122) &&
+               mbar_wait(&S->full[s], (it / STAGES) & 1, abort_flag, err, 122);
+          if (!ok) break;
+          fp8_fence_after();
+          const uint32_t sa = smem_u32(base + s * STAGE_BYTES), sb = sa + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            fp8_mma(tmem + b * BN, fp8_desc(sa + kk * 32), fp8_desc(sb + kk * 32), idesc, kk ? 1u : 0u);
+          fp8_commit(&S->empty[s]);
+          fp8_commit(&S->tfull[b]);
+        }
+      }
+    }
+  } else {   // -------------------------------------------------------- sums and output
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int r = q * 32 + lane;               // tile row of this thread
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+    const int NB = (p.N + kFp8Block - 1) / kFp8Block;
+    int it = 0, tl = 0;
+    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
+      int g, m, n;
+      decode(t, g, m, n);
+      const bool valid = r < S->rows[g] - m * BM;
+      const long long row = S->row_start[g] + (long long)m * BM + r;
+      long long arow = valid ? row : S->row_start[g];
+      if (MODE == 0) arow = groups.expert[g] < 0 ? arow - (long long)p.T * p.k : p.perm[arow] / p.k;
+      const float* sa = p.a_scales + arow * KB;
+      // weight scales: gate and up of the tile's block of I, or the block of this half
+      const long long wz = groups.z[g] * p.blob;
+      const int nb = MODE == 0 ? n : min(2 * n + half, NB - 1);
+      const float* sw0 = reinterpret_cast<const float*>(p.w_scales[0] + wz) + (long long)nb * KB;
+      const float* sw1 = reinterpret_cast<const float*>(p.w_scales[1] + wz) + (long long)nb * KB;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      bool ok = true;
+      float a = sa[0], w0 = sw0[0], w1 = MODE == 0 ? sw1[0] : 0.f;
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int b = it & 1;
+        const uint64_t f0 = pack_pair(a * w0, a * w0), f1 = MODE == 0 ? pack_pair(a * w1, a * w1) : f0;
+        if (kb + 1 < KB) {
+          a = sa[kb + 1];
+          w0 = sw0[kb + 1];
+          if (MODE == 0) w1 = sw1[kb + 1];
+        }
+        ok = mbar_wait(&S->tfull[b], (it >> 1) & 1, abort_flag, err, 123);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        fp8_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // half h: columns 128 h + 32 c of a product tile; 64 h + 32 (c % 2) of gate (c < 2) and of up
+          const int colb = MODE == 0 ? (c >> 1) * (BN / 2) + half * 64 + (c & 1) * 32 : half * (BN / 2) + c * 32;
+          uint32_t v[32];
+          tmem_ld32(lane_base + b * BN + colb, v);
+          tmem_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma_pair(acc[c * 16 + i], v[2 * i], v[2 * i + 1], c < 2 ? f0 : f1);
+        }
+        fp8_fence_before();
+        mbar_arrive(&S->tempty[b]);
+      }
+      if (!ok) break;
+      if (MODE == 0) {
+        float h[64], mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          h[2 * i] = silu(pair_lo(acc[i])) * pair_lo(acc[32 + i]);
+          h[2 * i + 1] = silu(pair_hi(acc[i])) * pair_hi(acc[32 + i]);
+          mx = amax_nan(amax_nan(mx, h[2 * i]), h[2 * i + 1]);
+        }
+        S->amax[tl & 1][half][r] = mx;
+        mbar_arrive(&S->halves);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&S->halves, tl & 1, abort_flag, err, 124));
+        if (!ok) break;
+        mx = amax_nan(mx, S->amax[tl & 1][half ^ 1][r]);
+        const float sc = fp8_scale(mx), inv = 1.0f / sc;
+        if (valid) {
+          const int c0 = n * TN + half * 64;
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + row * p.N + c0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c0 + 16 * j < p.N) {   // N is a multiple of 16
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float* v = h + 16 * j + 4 * i;
+                w[i] = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+              }
+              *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          if (half == 0) p.out_scales[row * NB + n] = sc;
+        }
+      } else if (valid) {
+        const int c0 = n * TN + half * (BN / 2);
+        const bool wide = p.out_bf16 ? (p.ldo % 8 == 0 && ((uintptr_t)p.out & 15) == 0)
+                                     : (p.ldo % 4 == 0 && ((uintptr_t)p.out & 15) == 0);
+        if (p.out_bf16) {
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.ldo + c0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {   // 8 columns
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16x2(pair_lo(acc[4 * j + i]), pair_hi(acc[4 * j + i]));
+            if (wide && c0 + 8 * j + 8 <= p.N) {
+              *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c0 + 8 * j + i < p.N) dst[8 * j + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
+          }
+        } else {
+          float* dst = static_cast<float*>(p.out) + row * p.ldo + c0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {   // 4 columns
+            const float v[4] = {pair_lo(acc[2 * j]), pair_hi(acc[2 * j]), pair_lo(acc[2 * j + 1]),
+                                pair_hi(acc[2 * j + 1])};
+            if (wide && c0 + 4 * j + 4 <= p.N) {
+              *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (c0 + 4 * j + i < p.N) dst[4 * j + i] = v[i];
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+  fp8_fence_before();
+  __syncthreads();
+  fp8_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
+}
+
+constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Smem);
+
+template <int MODE>
+cudaError_t launch_mode(const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  fp8_gemm_kernel<MODE><<<grid, THREADS, kSmemBytes, s>>>(maps, groups, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int num_sms,
+                            cudaStream_t s) {
+  if (groups.n <= 0 || p.T <= 0 || p.N <= 0) return cudaSuccess;
+  // an upper bound of the tile count (the groups' sizes are on the device); CTAs beyond the
+  // real count leave at once
+  const int tn = mode == 0 ? BN / 2 : BN;
+  const long long tiles = (((long long)p.T * p.k + p.T + BM - 1) / BM + groups.n) * ((p.N + tn - 1) / tn);
+  const int grid = (int)(tiles < num_sms ? tiles : num_sms);
+  return mode == 0 ? launch_mode<0>(maps, groups, p, grid, s) : launch_mode<1>(maps, groups, p, grid, s);
+}
+
+bool encode_map_fp8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
+                    uint64_t depth, uint64_t depth_bytes, uint32_t box_rows) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!fn) return false;
+  const cuuint32_t dim = depth > 0 ? 3 : 2;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {row_bytes, depth_bytes};
+  cuuint32_t box[3] = {(cuuint32_t)kFp8Block, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, dim, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace ftk
