@@ -12,16 +12,20 @@
 // registers.  A thread owns one row, so the factor sa * sw is one number for all its columns.
 //
 // One persistent kernel, one CTA per SM, 128 x 256 tiles:
-//   warp 0     TMA producer: per 128 of K, A 128 rows (gate/up: the pairs' token rows, gathered
-//              four at a time) and 256 weight rows, 128-byte swizzle, 4 stages of 48 KB.
-//   warp 1     MMA issuer: tcgen05.mma kind::f8f6f4, M=128, N=256, K=32, into two TMEM buffers
-//              of 256 columns in turn, so the tensor cores fill one while the other is read.
-//   warps 2-9  sums: warp w reads TMEM lanes 32 (w % 4).. of one half of the columns, adds
-//              them to 128 sums per thread, and at the end of a tile stores them.
+//   warp 0      TMA producer: per 128 of K, A 128 rows (gate/up: the pairs' token rows, gathered
+//               four at a time) and 256 weight rows, 128-byte swizzle, 4 stages of 48 KB.
+//   warp 1      MMA issuer: tcgen05.mma kind::f8f6f4, M=128, N=256, K=32, into two TMEM buffers
+//               of 256 columns in turn, so the tensor cores fill one while the other is read.
+//   warps 2, 3  factors: sa * sw of every row for 8 blocks of K at a time, into shared memory.
+//               (Read from global memory by the summing threads, the row scales' 32 separate
+//               lines per warp cost half of their time.)
+//   warps 4-11  sums: warp w reads TMEM lanes 32 (w % 4).. of one half of the columns, adds
+//               them to 128 sums per thread, and at the end of a tile stores them.  These warps
+//               take 216 registers each from the 168 of the launch, the other four keep 72.
 // gate/up tiles hold 128 gate and 128 up columns; each half of the warps takes 64 columns of
 // both, so silu(gate) * up stays inside a thread.
 //
-// Every wait is bounded: a thread that gives up records 121-124 in *err and raises the CTA's
+// Every wait is bounded: a thread that gives up records 121-125 in *err and raises the CTA's
 // abort flag; all roles then leave and TMEM is released.
 #include "fp8.hpp"
 #include "fp8_common.cuh"
@@ -33,17 +37,43 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = kFp8Block;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4, TMEM_COLS = 512;
-constexpr int SUM_WARPS = 8, THREADS = 64 + 32 * SUM_WARPS;
+constexpr int SUM_WARPS = 8, THREADS = 128 + 32 * SUM_WARPS;
+constexpr int FK = 8;   // blocks of K per chunk of factors
+// registers: (4 * 72 + 8 * 216) * 32 = 384 * 168, the launch's
+#define FP8_GEMM_CONTROL_REGS 72
+#define FP8_GEMM_SUM_REGS 216
 
 struct Smem {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], halves;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], ffull[2], fempty[2], halves;
   uint32_t tmem_base;
   int abort;
   int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
   int row_start[kMaxList];
   int rows[kMaxList];
   float amax[2][2][BM];         // gate/up: a row's largest |h| per half, double-buffered by tile
+  float factor[2][FK][2][BM];   // sa * sw of a row: by half of the columns, or for gate and up
 };
+
+// Eight words to a 32-byte aligned address.
+FT_DEVICE void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// v[i] of lane l <-> v[l] of lane i.
+FT_DEVICE void transpose32(uint32_t (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(i & o)) {   // trade v[i] of the upper lane for v[i + o] of the lower
+        const uint32_t give = up ? v[i] : v[i + o];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        if (up) v[i] = got; else v[i + o] = got;
+      }
+  }
+}
 
 template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -71,7 +101,9 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S->tfull[b], 1);
-      mbar_init(&S->tempty[b], 32 * SUM_WARPS);
+      mbar_init(&S->tempty[b], SUM_WARPS);
+      mbar_init(&S->ffull[b], 64);
+      mbar_init(&S->fempty[b], SUM_WARPS);
     }
     mbar_init(&S->halves, 32 * SUM_WARPS);
     S->abort = 0;
@@ -120,6 +152,8 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     m = (int)(local - (long long)n * mtg);
   };
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8_GEMM_CONTROL_REGS));
   if (warp == 0) {   // ------------------------------------------------ TMA producer
     int it = 0;
     for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
@@ -180,54 +214,104 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         }
       }
     }
+  } else {   // ---------------------------------------------------------- factors
+    const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
+    const int NB = (p.N + kFp8Block - 1) / kFp8Block;
+    int ch = 0;
+    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+      int g, m, n;
+      decode(t, g, m, n);
+      const int first = S->row_start[g], last = first + S->rows[g] - 1;
+      const float* sa[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {   // rows past the group repeat its last
+        int row = min(first + m * BM + r0 + 64 * i, last);
+        if (MODE == 0) row = groups.expert[g] < 0 ? row - p.T * p.k : p.perm[row] / p.k;
+        sa[i] = p.a_scales + (long long)row * KB;
+      }
+      // weight scales: gate and up of the tile's block of I, or the blocks of the tile's two halves
+      const long long wz = groups.z[g] * p.blob;
+      const float* sw[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)(MODE == 0 ? n : min(2 * n + i, NB - 1)) * KB;
+      bool ok = true;
+      for (int k0 = 0; k0 < KB; k0 += FK, ++ch) {
+        const int b = ch & 1, kn = min(FK, KB - k0);
+        float w[2][FK], a[2][FK];
+#pragma unroll
+        for (int j = 0; j < FK; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
+            a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
+          }
+        ok = mbar_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < FK; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            S->factor[b][j][0][r0 + 64 * i] = a[i][j] * w[0][j];
+            S->factor[b][j][1][r0 + 64 * i] = a[i][j] * w[1][j];
+          }
+        mbar_arrive(&S->ffull[b]);
+      }
+      if (!ok) break;
+    }
+  }
   } else {   // -------------------------------------------------------- sums and output
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8_GEMM_SUM_REGS));
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const int r = q * 32 + lane;               // tile row of this thread
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const int NB = (p.N + kFp8Block - 1) / kFp8Block;
-    int it = 0, tl = 0;
+    // half h sums columns 128 h .. of a product tile; columns 64 h .. of gate and of up
+    const uint32_t col0 = lane_base + half * (MODE == 0 ? 64 : BN / 2);
+    constexpr uint32_t HOP = MODE == 0 ? BN / 2 : 64;   // from the first 64 of its columns to the other 64
+    int it = 0, tl = 0, ch = 0;
     for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
       int g, m, n;
       decode(t, g, m, n);
       const bool valid = r < S->rows[g] - m * BM;
       const long long row = S->row_start[g] + (long long)m * BM + r;
-      long long arow = valid ? row : S->row_start[g];
-      if (MODE == 0) arow = groups.expert[g] < 0 ? arow - (long long)p.T * p.k : p.perm[arow] / p.k;
-      const float* sa = p.a_scales + arow * KB;
-      // weight scales: gate and up of the tile's block of I, or the block of this half
-      const long long wz = groups.z[g] * p.blob;
-      const int nb = MODE == 0 ? n : min(2 * n + half, NB - 1);
-      const float* sw0 = reinterpret_cast<const float*>(p.w_scales[0] + wz) + (long long)nb * KB;
-      const float* sw1 = reinterpret_cast<const float*>(p.w_scales[1] + wz) + (long long)nb * KB;
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       bool ok = true;
-      float a = sa[0], w0 = sw0[0], w1 = MODE == 0 ? sw1[0] : 0.f;
       for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int b = it & 1;
-        const uint64_t f0 = pack_pair(a * w0, a * w0), f1 = MODE == 0 ? pack_pair(a * w1, a * w1) : f0;
-        if (kb + 1 < KB) {
-          a = sa[kb + 1];
-          w0 = sw0[kb + 1];
-          if (MODE == 0) w1 = sw1[kb + 1];
-        }
-        ok = mbar_wait(&S->tfull[b], (it >> 1) & 1, abort_flag, err, 123);
+        const int b = it & 1, j = kb % FK, fb = ch & 1;
+        if (j == 0) ok = mbar_wait(&S->ffull[fb], (ch >> 1) & 1, abort_flag, err, 123);
+        ok = ok && mbar_wait(&S->tfull[b], (it >> 1) & 1, abort_flag, err, 123);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         fp8_fence_after();
+        const uint32_t ta = col0 + b * BN;
+        uint32_t v0[32], v1[32];
+        tmem_ld32(ta, v0);
+        const float x0 = S->factor[fb][j][MODE == 0 ? 0 : half][r], x1 = MODE == 0 ? S->factor[fb][j][1][r] : x0;
+        const uint64_t f0 = pack_pair(x0, x0), f1 = pack_pair(x1, x1);
+        tmem_wait();
+        tmem_ld32(ta + 32, v1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // half h: columns 128 h + 32 c of a product tile; 64 h + 32 (c % 2) of gate (c < 2) and of up
-          const int colb = MODE == 0 ? (c >> 1) * (BN / 2) + half * 64 + (c & 1) * 32 : half * (BN / 2) + c * 32;
-          uint32_t v[32];
-          tmem_ld32(lane_base + b * BN + colb, v);
-          tmem_wait();
+        for (int i = 0; i < 16; ++i) fma_pair(acc[i], v0[2 * i], v0[2 * i + 1], f0);
+        tmem_wait();
+        tmem_ld32(ta + HOP, v0);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma_pair(acc[c * 16 + i], v[2 * i], v[2 * i + 1], c < 2 ? f0 : f1);
-        }
+        for (int i = 0; i < 16; ++i) fma_pair(acc[16 + i], v1[2 * i], v1[2 * i + 1], f0);
+        tmem_wait();
+        tmem_ld32(ta + HOP + 32, v1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma_pair(acc[32 + i], v0[2 * i], v0[2 * i + 1], f1);
+        tmem_wait();
         fp8_fence_before();
-        mbar_arrive(&S->tempty[b]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S->tempty[b]);   // every lane's values are in registers
+        const bool chunk_done = j == FK - 1 || kb == KB - 1;
+        if (chunk_done && lane == 0) mbar_arrive(&S->fempty[fb]);
+        ch += chunk_done;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma_pair(acc[48 + i], v1[2 * i], v1[2 * i + 1], f1);
       }
       if (!ok) break;
       if (MODE == 0) {
@@ -260,37 +344,52 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
             }
           if (half == 0) p.out_scales[row * NB + n] = sc;
         }
-      } else if (valid) {
+      } else {
         const int c0 = n * TN + half * (BN / 2);
-        const bool wide = p.out_bf16 ? (p.ldo % 8 == 0 && ((uintptr_t)p.out & 15) == 0)
-                                     : (p.ldo % 4 == 0 && ((uintptr_t)p.out & 15) == 0);
-        if (p.out_bf16) {
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.ldo + c0;
+        const int es = p.out_bf16 ? 2 : 4;
+        unsigned char* dst = static_cast<unsigned char*>(p.out) + (row * p.ldo + c0) * es;
+        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + BN / 2 <= p.N) {
+          // a thread stores its own row, a whole 32-byte sector at a time
+          if (valid) {
+            if (p.out_bf16) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {   // 8 columns
-            uint32_t w[4];
+              for (int j = 0; j < 8; ++j) {
+                uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = bf16x2(pair_lo(acc[4 * j + i]), pair_hi(acc[4 * j + i]));
-            if (wide && c0 + 8 * j + 8 <= p.N) {
-              *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 8; ++i) w[i] = bf16x2(pair_lo(acc[8 * j + i]), pair_hi(acc[8 * j + i]));
+                st_sector(dst + 32 * j, w);
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (c0 + 8 * j + i < p.N) dst[8 * j + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+              for (int j = 0; j < 16; ++j) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = (uint32_t)(acc[4 * j + (i >> 1)] >> (32 * (i & 1)));
+                st_sector(dst + 32 * j, w);
+              }
             }
           }
         } else {
-          float* dst = static_cast<float*>(p.out) + row * p.ldo + c0;
+          // any other row: the warp transposes 32 x 32 values, so that its lanes store 32
+          // consecutive columns of a row
+          const int rows_left = S->rows[g] - m * BM - q * 32;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {   // 4 columns
-            const float v[4] = {pair_lo(acc[2 * j]), pair_hi(acc[2 * j]), pair_lo(acc[2 * j + 1]),
-                                pair_hi(acc[2 * j + 1])};
-            if (wide && c0 + 4 * j + 4 <= p.N) {
-              *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v[32];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (c0 + 4 * j + i < p.N) dst[4 * j + i] = v[i];
+            for (int i = 0; i < 32; ++i) v[i] = (uint32_t)(acc[16 * j + (i >> 1)] >> (32 * (i & 1)));
+            transpose32(v, lane);
+            const int col = c0 + 32 * j + lane;
+            if (col < p.N) {
+              const long long at = (row - lane) * p.ldo + col;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < rows_left) {
+                  if (p.out_bf16)
+                    static_cast<uint16_t*>(p.out)[at + i * p.ldo] = (uint16_t)bf16x2(__uint_as_float(v[i]), 0.f);
+                  else
+                    static_cast<uint32_t*>(p.out)[at + i * p.ldo] = v[i];
+                }
             }
           }
         }
