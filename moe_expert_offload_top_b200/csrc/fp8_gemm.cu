@@ -44,7 +44,7 @@ constexpr int FK = 8;   // blocks of K per chunk of factors
 #define FP8_GEMM_SUM_REGS 216
 
 struct Smem {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], ffull[2], fempty[2], halves;
+  uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves;
   uint32_t tmem_base;
   int abort;
   int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
@@ -97,10 +97,9 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&S->full[s], 1);
-      mbar_init(&S->empty[s], 1);
+      mbar_init(&S->done[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&S->tfull[b], 1);
       mbar_init(&S->tempty[b], SUM_WARPS);
       mbar_init(&S->ffull[b], 64);
       mbar_init(&S->fempty[b], SUM_WARPS);
@@ -176,7 +175,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         unsigned char* sa = base + s * STAGE_BYTES;
         unsigned char* sb = sa + A_BYTES;
         if (lane == 0) {
-          ok = mbar_wait(&S->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121);
+          ok = pipe_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121);
           if (ok) {
             mbar_expect_tx(&S->full[s], STAGE_BYTES);
             if (MODE == 1) fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
@@ -193,25 +192,26 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     }
     // drain: wait (bounded) until every issued stage has landed
     for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
-  } else if (warp == 1) {
-    if (lane == 0) {   // ---------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = fp8_idesc(BM, BN);
-      int it = 0;
-      bool ok = true;
-      for (long long t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = it % STAGES, b = it & 1;
-          ok = mbar_wait(&S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122) &&
-               mbar_wait(&S->full[s], (it / STAGES) & 1, abort_flag, err, 122);
-          if (!ok) break;
-          fp8_fence_after();
-          const uint32_t sa = smem_u32(base + s * STAGE_BYTES), sb = sa + A_BYTES;
+  } else if (warp == 1) {   // ------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = fp8_idesc(BM, BN);
+    const uint64_t desc0 = fp8_desc(smem_u32(base));   // stage s, K step kk: + (s * STAGE_BYTES + kk * 32) / 16
+    int it = 0;
+    bool ok = true;
+    for (long long t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int s = it % STAGES, b = it & 1;
+        ok = pipe_wait(&S->full[s], (it / STAGES) & 1, abort_flag, err, 122) &&
+             pipe_wait(&S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        fp8_fence_after();
+        if (elect_one()) {
+          const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            fp8_mma(tmem + b * BN, fp8_desc(sa + kk * 32), fp8_desc(sb + kk * 32), idesc, kk ? 1u : 0u);
-          fp8_commit(&S->empty[s]);
-          fp8_commit(&S->tfull[b]);
+          for (int kk = 0; kk < BK / 32; ++kk) fp8_mma(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+          fp8_commit(&S->done[s]);   // frees the stage and hands the buffer to the sums
         }
+        __syncwarp();
       }
     }
   } else {   // ---------------------------------------------------------- factors
@@ -246,7 +246,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
             w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
             a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
           }
-        ok = mbar_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
+        ok = pipe_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < FK; ++j)
@@ -275,34 +275,41 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       decode(t, g, m, n);
       const bool valid = r < S->rows[g] - m * BM;
       const long long row = S->row_start[g] + (long long)m * BM + r;
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      bool ok = true;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      // The next block's first columns are asked for before this one's last are added, so that
+      // the wait for the tensor cores and the load's latency pass behind multiply-adds.
+      uint32_t v0[32], v1[32];
+      auto ready = [&](int i) {   // accumulators of block i (over the tiles)
+        const bool w = pipe_wait(&S->done[i % STAGES], (i / STAGES) & 1, abort_flag, err, 123);
+        const bool all = __all_sync(0xFFFFFFFFu, w);
+        fp8_fence_after();
+        return all;
+      };
+      bool ok = ready(it);
+      if (!ok) break;
+      tmem_ld32(col0 + (it & 1) * BN, v0);
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int b = it & 1, j = kb % FK, fb = ch & 1;
-        if (j == 0) ok = mbar_wait(&S->ffull[fb], (ch >> 1) & 1, abort_flag, err, 123);
-        ok = ok && mbar_wait(&S->tfull[b], (it >> 1) & 1, abort_flag, err, 123);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        fp8_fence_after();
+        if (j == 0) {
+          ok = __all_sync(0xFFFFFFFFu, pipe_wait(&S->ffull[fb], (ch >> 1) & 1, abort_flag, err, 123));
+          if (!ok) break;
+        }
         const uint32_t ta = col0 + b * BN;
-        uint32_t v0[32], v1[32];
-        tmem_ld32(ta, v0);
-        const float x0 = S->factor[fb][j][MODE == 0 ? 0 : half][r], x1 = MODE == 0 ? S->factor[fb][j][1][r] : x0;
-        const uint64_t f0 = pack_pair(x0, x0), f1 = pack_pair(x1, x1);
+        const float f0 = S->factor[fb][j][MODE == 0 ? 0 : half][r], f1 = MODE == 0 ? S->factor[fb][j][1][r] : f0;
         tmem_wait();
         tmem_ld32(ta + 32, v1);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma_pair(acc[i], v0[2 * i], v0[2 * i + 1], f0);
+        for (int i = 0; i < 32; ++i) fma_col(acc[i], v0[i], f0);
         tmem_wait();
         tmem_ld32(ta + HOP, v0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma_pair(acc[16 + i], v1[2 * i], v1[2 * i + 1], f0);
+        for (int i = 0; i < 32; ++i) fma_col(acc[32 + i], v1[i], f0);
         tmem_wait();
         tmem_ld32(ta + HOP + 32, v1);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma_pair(acc[32 + i], v0[2 * i], v0[2 * i + 1], f1);
+        for (int i = 0; i < 32; ++i) fma_col(acc[64 + i], v0[i], f1);
         tmem_wait();
         fp8_fence_before();
         __syncwarp();
@@ -310,21 +317,25 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         const bool chunk_done = j == FK - 1 || kb == KB - 1;
         if (chunk_done && lane == 0) mbar_arrive(&S->fempty[fb]);
         ch += chunk_done;
+        if (kb + 1 < KB) {
+          ok = ready(it + 1);
+          if (!ok) break;
+          tmem_ld32(col0 + (b ^ 1) * BN, v0);
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma_pair(acc[48 + i], v1[2 * i], v1[2 * i + 1], f1);
+        for (int i = 0; i < 32; ++i) fma_col(acc[96 + i], v1[i], f1);
       }
       if (!ok) break;
       if (MODE == 0) {
         float h[64], mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          h[2 * i] = silu(pair_lo(acc[i])) * pair_lo(acc[32 + i]);
-          h[2 * i + 1] = silu(pair_hi(acc[i])) * pair_hi(acc[32 + i]);
-          mx = amax_nan(amax_nan(mx, h[2 * i]), h[2 * i + 1]);
+        for (int i = 0; i < 64; ++i) {
+          h[i] = silu(acc[i]) * acc[64 + i];
+          mx = amax_nan(mx, h[i]);
         }
         S->amax[tl & 1][half][r] = mx;
         mbar_arrive(&S->halves);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&S->halves, tl & 1, abort_flag, err, 124));
+        ok = __all_sync(0xFFFFFFFFu, pipe_wait(&S->halves, tl & 1, abort_flag, err, 124));
         if (!ok) break;
         mx = amax_nan(mx, S->amax[tl & 1][half ^ 1][r]);
         const float sc = fp8_scale(mx), inv = 1.0f / sc;
@@ -356,7 +367,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               for (int j = 0; j < 8; ++j) {
                 uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = bf16x2(pair_lo(acc[8 * j + i]), pair_hi(acc[8 * j + i]));
+                for (int i = 0; i < 8; ++i) w[i] = bf16x2(acc[16 * j + 2 * i], acc[16 * j + 2 * i + 1]);
                 st_sector(dst + 32 * j, w);
               }
             } else {
@@ -364,7 +375,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               for (int j = 0; j < 16; ++j) {
                 uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = (uint32_t)(acc[4 * j + (i >> 1)] >> (32 * (i & 1)));
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[8 * j + i]);
                 st_sector(dst + 32 * j, w);
               }
             }
@@ -377,7 +388,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
           for (int j = 0; j < 4; ++j) {
             uint32_t v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = (uint32_t)(acc[16 * j + (i >> 1)] >> (32 * (i & 1)));
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);
             transpose32(v, lane);
             const int col = c0 + 32 * j + lane;
             if (col < p.N) {

@@ -29,6 +29,21 @@ FT_DEVICE void fp8_tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
       : "memory");
 }
 
+// mbar_wait for the pipelines below: the clock is read only once a wait has lasted a while.
+FT_DEVICE bool pipe_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try(b, parity)) return true;
+  return mbar_wait(b, parity, abort_flag, err, code);
+}
+
+// One lane of a converged warp.  The compiler then knows that what follows runs in one thread,
+// and issues tcgen05 instructions with warp-uniform operands once instead of in a loop over lanes.
+FT_DEVICE bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
 FT_DEVICE uint64_t fp8_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
@@ -67,16 +82,9 @@ FT_DEVICE void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 FT_DEVICE void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// acc (two fp32) += v (two fp32) * s (two fp32), each product rounded once with its sum.
-// volatile: stays behind the wait for the accumulators it reads.
-FT_DEVICE void fma_pair(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
-  asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-               : "+l"(acc) : "r"(v0), "r"(v1), "l"(s));
+// acc += v * s, rounded once.  volatile: stays behind the wait for the accumulator column v.
+FT_DEVICE void fma_col(float& acc, uint32_t v, float s) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
-FT_DEVICE uint64_t pack_pair(float a, float b) {
-  return (uint64_t)__float_as_uint(a) | (uint64_t)__float_as_uint(b) << 32;
-}
-FT_DEVICE float pair_lo(uint64_t p) { return __uint_as_float((uint32_t)p); }
-FT_DEVICE float pair_hi(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
 
 }  // namespace ftk
