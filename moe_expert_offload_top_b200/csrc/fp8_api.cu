@@ -152,7 +152,7 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   const size_t sb = 4 * (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
   ftk::Fp8Maps up, down;
-  if (!ftk::encode_map_fp8(&up.a, x, H, T, ldx, 0, 0, 1) ||
+  if (!ftk::encode_map_fp8(&up.a, y, H, rows, 4ull * H, 0, 0, 128) ||
       !ftk::encode_map_fp8(&up.b[0], w, H, I, H, n_slots, blob, 128) ||
       !ftk::encode_map_fp8(&up.b[1], w + n, H, I, H, n_slots, blob, 128) ||
       !ftk::encode_map_fp8(&down.a, h, I, rows, I, 0, 0, 128) ||
@@ -167,7 +167,9 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
                        y, nullptr, H, 0, err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = num_sms();
-  cudaError_t e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
+  // the pairs' token rows wait in the rows of y that the down product writes last
+  cudaError_t e = ftk::launch_fp8_gather(x, ldx, groups, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
+  if (e == cudaSuccess) e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
   if (e == cudaSuccess) e = ftk::launch_fp8_gemm(1, down, groups, d, sms, s);
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }

@@ -12,8 +12,10 @@
 // registers.  A thread owns one row, so the factor sa * sw is one number for all its columns.
 //
 // One persistent kernel, one CTA per SM, 128 x 256 tiles:
-//   warp 0      TMA producer: per 128 of K, A 128 rows (gate/up: the pairs' token rows, gathered
-//               four at a time) and 256 weight rows, 128-byte swizzle, 4 stages of 48 KB.
+//   warp 0      TMA producer: per 128 of K, A 128 rows and 256 weight rows, 128-byte swizzle, 4
+//               stages of 48 KB.  (Gathering the pairs' token rows here, four per TMA load,
+//               took twice the time of the products: 32 loads to issue per stage instead of
+//               one.  fp8_gather_kernel copies them first.)
 //   warp 1      MMA issuer: tcgen05.mma kind::f8f6f4, M=128, N=256, K=32, into two TMEM buffers
 //               of 256 columns in turn, so the tensor cores fill one while the other is read.
 //   warps 2, 3  factors: sa * sw of every row for 8 blocks of K at a time, into shared memory.
@@ -159,34 +161,22 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       int g, m, n;
       decode(t, g, m, n);
       const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
-      int tok[4];
-      if (MODE == 0) {   // lane l gathers tile rows 4l .. 4l+3; rows past the group repeat its last
-        const int last = S->row_start[g] + S->rows[g] - 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int q = min(row0 + 4 * lane + i, last);
-          tok[i] = groups.expert[g] < 0 ? q - p.T * p.k : p.perm[q] / p.k;
-        }
-      }
       bool stop = false;
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int s = it % STAGES;
-        bool ok = true;
-        unsigned char* sa = base + s * STAGE_BYTES;
-        unsigned char* sb = sa + A_BYTES;
-        if (lane == 0) {
-          ok = pipe_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121);
-          if (ok) {
-            mbar_expect_tx(&S->full[s], STAGE_BYTES);
-            if (MODE == 1) fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
-            fp8_tma_3d(sb, &maps.b[0], &S->full[s], kb * BK, n * TN, z);
-            fp8_tma_3d(sb + B_BYTES / 2, &maps.b[1], &S->full[s], kb * BK, MODE == 0 ? n * TN : n * TN + BN / 2, z);
-          }
+        if (!__all_sync(0xFFFFFFFFu, pipe_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121))) {
+          stop = true;
+          break;
         }
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) { stop = true; break; }
-        if (MODE == 0)
-          fp8_tma_gather4(sa + lane * 4 * BK, &maps.a, &S->full[s], kb * BK, tok[0], tok[1], tok[2], tok[3]);
+        if (elect_one()) {
+          unsigned char* sa = base + s * STAGE_BYTES;
+          unsigned char* sb = sa + A_BYTES;
+          mbar_expect_tx(&S->full[s], STAGE_BYTES);
+          fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
+          fp8_tma_3d(sb, &maps.b[0], &S->full[s], kb * BK, n * TN, z);
+          fp8_tma_3d(sb + B_BYTES / 2, &maps.b[1], &S->full[s], kb * BK, MODE == 0 ? n * TN : n * TN + BN / 2, z);
+        }
+        __syncwarp();
       }
       if (stop) break;
     }
@@ -415,6 +405,21 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
 }
 
+// The token row of every listed pair, H bytes (a multiple of 16) at dst + pair * stride.
+// One warp per row; bound by memory (the reads hit the L2).
+__global__ void __launch_bounds__(256) fp8_gather_kernel(const uint8_t* x, long long ldx, const __grid_constant__ GemmGroups groups,
+                                                         const int* offsets, const int* perm, int T, int k, int H,
+                                                         uint8_t* dst, long long stride) {
+  const int g = blockIdx.y, e = groups.expert[g], lane = threadIdx.x & 31;
+  const int first = e >= 0 ? offsets[e] : T * k, last = e >= 0 ? offsets[e + 1] : T * k + T;
+  for (int q = first + blockIdx.x * 8 + (threadIdx.x >> 5); q < last; q += gridDim.x * 8) {
+    const int tok = e >= 0 ? perm[q] / k : q - T * k;
+    const uint4* from = reinterpret_cast<const uint4*>(x + tok * ldx);
+    uint4* to = reinterpret_cast<uint4*>(dst + q * stride);
+    for (int i = lane; i < H / 16; i += 32) to[i] = from[i];
+  }
+}
+
 constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Smem);
 
 template <int MODE>
@@ -437,6 +442,18 @@ cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& gro
   const long long tiles = (((long long)p.T * p.k + p.T + BM - 1) / BM + groups.n) * ((p.N + tn - 1) / tn);
   const int grid = (int)(tiles < num_sms ? tiles : num_sms);
   return mode == 0 ? launch_mode<0>(maps, groups, p, grid, s) : launch_mode<1>(maps, groups, p, grid, s);
+}
+
+cudaError_t launch_fp8_gather(const void* x, long long ldx, const GemmGroups& groups, const int* offsets,
+                              const int* perm, int T, int k, int H, void* dst, long long stride, int num_sms,
+                              cudaStream_t s) {
+  if (groups.n <= 0 || T <= 0) return cudaSuccess;
+  // enough warps to fill the SMs, split evenly over the groups; none beyond a group's possible rows
+  const int want = (8 * num_sms + groups.n - 1) / groups.n, most = (T + 7) / 8;
+  const dim3 grid(want < most ? want : most, groups.n);
+  fp8_gather_kernel<<<grid, 256, 0, s>>>(static_cast<const uint8_t*>(x), ldx, groups, offsets, perm, T, k, H,
+                                         static_cast<uint8_t*>(dst), stride);
+  return cudaGetLastError();
 }
 
 bool encode_map_fp8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
