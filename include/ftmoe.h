@@ -586,7 +586,7 @@ FT_API int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, i
  *   nearest even) if out_is_bf16 else f32.  Any M, N and K >= 1; lda and ldw multiples of 16,
  *   a and w 16-byte aligned; bytes past K of a row are not read as values.
  *   err: a DEVICE int, 0 before the call; a kernel whose bounded pipeline wait gives up writes
- *   121-125 there (the outputs are then incomplete). */
+ *   121-129 there (the outputs are then incomplete). */
 FT_API int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
                        const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
                        void* stream);

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libftmoe.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "router.cu", "permute.cu", "expert_decode.cu", "grouped_gemm_sm100.cu", "noalloc.cu",
            "ffn_fused_f32.cu", "ffn_fused_bf16.cu", "ffn_fused_int4.cu", "ffn_fused_nvfp4.cu", "gemv_int4_mma.cu",
-           "gemv_nvfp4_mma.cu", "gemv_bf16_mma.cu", "rows_fp8.cu", "fp8_gemm.cu", "fp8_api.cu"]
+           "gemv_nvfp4_mma.cu", "gemv_bf16_mma.cu", "rows_fp8.cu", "fp8_gemm.cu", "fp8_stream.cu",
+           "fp8_api.cu"]
 HEADERS = ["common.cuh", "kernels.hpp", "cache.hpp", "sm100_sync.cuh", "decode_gemv.cuh", "ffn_fused.cuh",
            "gemv_ring.cuh", "fp8.hpp", "fp8_common.cuh", "fp8_mma.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

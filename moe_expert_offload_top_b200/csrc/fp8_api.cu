@@ -43,6 +43,24 @@ int num_sms() {
   return n;
 }
 
+// How a product of `rows` rows per group runs: nt > 0 on the streaming kernel with nt tokens per
+// CTA, nt = 0 on the tiles of 128 rows.
+struct Plan {
+  int nt, split, chunks;
+};
+Plan plan(int mode, long long rows, int groups, int N, int K, int sms) {
+  Plan pl{0, 1, 1};
+  if (rows > (mode == 0 ? 64 : 256)) return pl;
+  const int most = mode == 0 ? 64 : 128;
+  pl.nt = 16;
+  while (pl.nt < rows && pl.nt < most) pl.nt *= 2;
+  pl.chunks = (int)((rows + pl.nt - 1) / pl.nt);
+  const long long tiles = (long long)ftk::fp8_blocks(N) * groups * pl.chunks;
+  const int kb = ftk::fp8_blocks(K);
+  while (pl.split < 8 && tiles * pl.split < 2 * sms && kb >= 4 * pl.split) pl.split *= 2;
+  return pl;
+}
+
 int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stream) {
   const uintptr_t es = x_is_bf16 ? 2 : 4;
   if (p.T < 0 || p.H < 1) return bad(call, "invalid size");
@@ -95,8 +113,10 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
     return bad(call, "a buffer is not aligned to its elements");
   const int rc = check_device(call, out);
   if (rc != FT_OK) return rc;
+  const int sms = num_sms();
+  const Plan pl = plan(1, M, 1, N, K, sms);
   ftk::Fp8Maps m;
-  if (!ftk::encode_map_fp8(&m.a, a, K, M, lda, 0, 0, 128) ||
+  if (!ftk::encode_map_fp8(&m.a, a, K, M, lda, 0, 0, pl.nt ? pl.nt : 128) ||
       !ftk::encode_map_fp8(&m.b[0], w, K, N, ldw, 1, (uint64_t)ldw * N, 128)) {
     ftk::set_step_error(std::string(call) + ": cuTensorMapEncodeTiled failed");
     return FT_ERR_CUDA;
@@ -108,7 +128,9 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
   groups.z[0] = 0;
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(w_scales);
   const ftk::Fp8Gemm p{a_scales, {ws, ws}, 0, nullptr, nullptr, M, 0, N, K, out, nullptr, ldo, out_is_bf16 != 0, err};
-  const cudaError_t e = ftk::launch_fp8_gemm(1, m, groups, p, num_sms(), static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pl.nt ? ftk::launch_fp8_stream(1, pl.nt, pl.split, pl.chunks, m, groups, p, s)
+                              : ftk::launch_fp8_gemm(1, m, groups, p, sms, s);
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
 
@@ -151,11 +173,16 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   const uint64_t rows = (uint64_t)T * top_k + T, n = (uint64_t)H * I, blob = ft_fp8_blob_bytes(H, I);
   const size_t sb = 4 * (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
+  // pairs per listed expert, were they spread evenly
+  const int sms = num_sms();
+  const long long each = ((long long)T * top_k + n_list - 1) / n_list;
+  const Plan pu = plan(0, each, n_list, I, H, sms), pd = plan(1, each > 64 ? 257 : each, n_list, H, I, sms);
   ftk::Fp8Maps up, down;
-  if (!ftk::encode_map_fp8(&up.a, y, H, rows, 4ull * H, 0, 0, 128) ||
+  if (!(pu.nt ? ftk::encode_map_fp8(&up.a, x, H, T, ldx, 0, 0, 1)
+              : ftk::encode_map_fp8(&up.a, y, H, rows, 4ull * H, 0, 0, 128)) ||
       !ftk::encode_map_fp8(&up.b[0], w, H, I, H, n_slots, blob, 128) ||
       !ftk::encode_map_fp8(&up.b[1], w + n, H, I, H, n_slots, blob, 128) ||
-      !ftk::encode_map_fp8(&down.a, h, I, rows, I, 0, 0, 128) ||
+      !ftk::encode_map_fp8(&down.a, h, I, rows, I, 0, 0, pd.nt ? pd.nt : 128) ||
       !ftk::encode_map_fp8(&down.b[0], w + 2 * n, I, H, I, n_slots, blob, 128)) {
     ftk::set_step_error(std::string(call) + ": cuTensorMapEncodeTiled failed");
     return FT_ERR_CUDA;
@@ -166,11 +193,17 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   const ftk::Fp8Gemm d{h_scales, {ws + 2 * sb, ws + 2 * sb}, (long long)blob, offsets, perm, T, top_k, H, I,
                        y, nullptr, H, 0, err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = num_sms();
-  // the pairs' token rows wait in the rows of y that the down product writes last
-  cudaError_t e = ftk::launch_fp8_gather(x, ldx, groups, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
-  if (e == cudaSuccess) e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
-  if (e == cudaSuccess) e = ftk::launch_fp8_gemm(1, down, groups, d, sms, s);
+  cudaError_t e;
+  if (pu.nt) {
+    e = ftk::launch_fp8_stream(0, pu.nt, pu.split, pu.chunks, up, groups, g, s);
+  } else {
+    // the pairs' token rows wait in the rows of y that the down product writes last
+    e = ftk::launch_fp8_gather(x, ldx, groups, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
+    if (e == cudaSuccess) e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
+  }
+  if (e == cudaSuccess)
+    e = pd.nt ? ftk::launch_fp8_stream(1, pd.nt, pd.split, pd.chunks, down, groups, d, s)
+              : ftk::launch_fp8_gemm(1, down, groups, d, sms, s);
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
 

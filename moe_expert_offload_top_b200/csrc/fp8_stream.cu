@@ -1,0 +1,383 @@
+// Block-scaled fp8 products for few rows: bound by the weights' bytes.
+//
+// The same functions as fp8_gemm.cu with the operands changed over: 128 weight rows are the
+// M of a tcgen05.mma and up to NT token rows its N (16 .. 128), so that one token costs the
+// tensor cores N = 16 and not a tile of 128 rows.  TMEM lane = weight row, column = token:
+//
+//   acc[n][t] += sw[n / 128][kb] sa[t][kb] * (sum over k in block kb of w[n][k] a[t][k])
+//
+// One CTA per (128 weight rows, expert, NT tokens), two CTAs per SM where registers allow:
+//   warp 0     TMA producer: the weight tile(s) of a block of K (16 KB; gate and up 32 KB) and
+//              the tokens' 128 bytes each (gate/up: gathered four rows at a time), into a ring
+//              of about 100 KB per CTA.  The ring is what reaches the memory's rate: 200 KB in
+//              flight per SM.
+//   warp 1     MMA issuer, into TMEM buffers in turn (256 columns per CTA).
+//   warps 2,3  factors sa * sw of the tokens, four blocks of K at a time, into shared memory.
+//   others     sums: a thread owns a weight row; 16 columns at a time leave TMEM and are added
+//              with the columns' factors (the same for all lanes: broadcast reads).
+// Few tiles (a narrow product) leave SMs without weights to read, so K is split over the CTAs of
+// a cluster: each leaves its sums in its shared memory, and rank r adds the columns r * NT / S ..
+// of all ranks in rank order (the result does not depend on timing), and stores them.
+// Stores: 128 threads hold 128 consecutive columns of one output row.
+//
+// Every wait is bounded as in fp8_gemm.cu (codes 126-129); the cluster barriers are reached by
+// every thread whatever its role met.
+#include "fp8.hpp"
+#include "fp8_common.cuh"
+#include "fp8_mma.cuh"
+
+namespace ftk {
+namespace {
+
+constexpr int BK = kFp8Block, WTILE = 128 * BK;
+constexpr int FK = 4;             // blocks of K per chunk of factors
+constexpr int TMEM_COLS = 256;
+constexpr int MAX_STAGES = 8, MAX_BUFS = 8;
+
+template <int COLS, int NT>
+struct Ctrl {
+  uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_BUFS], ffull[2], fempty[2];
+  uint32_t tmem_base;
+  int abort;
+  alignas(16) float factor[2][FK][COLS];
+  float wmax[4][NT];              // gate/up: largest |h| of a token in each of the four warps
+};
+
+template <int MODE, int NT>
+struct Cfg {
+  static constexpr int W = MODE == 0 ? 2 : 1;           // weight tiles per block of K
+  static constexpr int COLS = W * NT;                   // accumulator columns
+  static constexpr int SW = COLS > 64 ? 2 : 1;          // summing warpgroups
+  static constexpr int THREADS = 128 + 128 * SW;
+  static constexpr int PER_SM = COLS > 64 ? 1 : 2;
+  static constexpr int STAGE = W * WTILE + NT * BK;
+  // shared memory of an SM (228 KB, 1 KB of it reserved per CTA) over its CTAs
+  static constexpr int LIMIT = (228 * 1024) / PER_SM - 1024;
+  static constexpr int FIT = (LIMIT - 1024 - (int)sizeof(Ctrl<COLS, NT>)) / STAGE;
+  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int BUFS = TMEM_COLS / COLS < MAX_BUFS ? TMEM_COLS / COLS : MAX_BUFS;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(Ctrl<COLS, NT>);
+  static_assert(STAGES * STAGE >= COLS * 128 * 4, "the sums of a tile wait in the ring's memory");
+};
+
+FT_DEVICE void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+FT_DEVICE void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float at this CTA's shared address, in the CTA `rank` of the cluster.
+FT_DEVICE float ld_rank(uint32_t addr, int rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(Cfg<MODE, NT>::THREADS, Cfg<MODE, NT>::PER_SM)
+fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ GemmGroups groups,
+                  const __grid_constant__ Fp8Gemm p, int split) {
+  using C = Cfg<MODE, NT>;
+  constexpr int W = C::W, COLS = C::COLS, STAGES = C::STAGES, BUFS = C::BUFS, STAGE = C::STAGE;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Ctrl<COLS, NT>* S = reinterpret_cast<Ctrl<COLS, NT>*>(base + STAGES * STAGE);
+  float* part = reinterpret_cast<float*>(base);   // [COLS][128] sums, once the ring is drained
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (p.K + BK - 1) / BK, NB = (p.N + BK - 1) / BK;
+  const int rank = split > 1 ? blockIdx.x % split : 0;
+  const int n = blockIdx.x / split, g = blockIdx.y;
+  const int kb0 = (int)((long long)KB * rank / split), kb1 = (int)((long long)KB * (rank + 1) / split);
+  const int e = groups.expert[g], z = groups.z[g];
+  const int first = e >= 0 ? p.offsets[e] : p.T * p.k;
+  const int rows = e >= 0 ? p.offsets[e + 1] - first : p.T;
+  // the same for every CTA of a cluster (they differ in blockIdx.x only)
+  if ((long long)blockIdx.z * NT >= rows) return;
+  int* err = p.err;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&S->full[s], 1);
+      mbar_init(&S->done[s], 1);
+    }
+    for (int b = 0; b < BUFS; ++b) mbar_init(&S->tempty[b], 4 * C::SW);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&S->ffull[b], 64);
+      mbar_init(&S->fempty[b], 4 * C::SW);
+    }
+    S->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&S->tmem_base)), "r"(TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fp8_fence_before();
+  __syncthreads();
+  fp8_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  volatile int* abort_flag = &S->abort;
+
+  int it = 0, ch = 0;   // blocks of K and chunks of factors so far
+  for (int t0 = blockIdx.z * NT; t0 < rows; t0 += gridDim.z * NT) {
+    const int valid = min(NT, rows - t0), row0 = first + t0;
+    if (warp == 0) {   // -------------------------------------------------- TMA producer
+      int tok[(NT + 31) / 32];
+      if (MODE == 0) {   // tokens past the last repeat it
+#pragma unroll
+        for (int i = 0; i < (NT + 31) / 32; ++i) {
+          const int q = row0 + min(i * 32 + lane, valid - 1);
+          tok[i] = e < 0 ? q - p.T * p.k : p.perm[q] / p.k;
+        }
+      }
+      int i = it;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % STAGES;
+        if (!__all_sync(0xFFFFFFFFu, pipe_wait(&S->done[s], ((i / STAGES) & 1) ^ 1, abort_flag, err, 126))) break;
+        unsigned char* sw = base + s * STAGE;
+        if (elect_one()) {
+          mbar_expect_tx(&S->full[s], STAGE);
+          fp8_tma_3d(sw, &maps.b[0], &S->full[s], kb * BK, n * 128, z);
+          if (W == 2) fp8_tma_3d(sw + WTILE, &maps.b[1], &S->full[s], kb * BK, n * 128, z);
+          if (MODE == 1) fp8_tma_2d(sw + W * WTILE, &maps.a, &S->full[s], kb * BK, row0);
+        }
+        __syncwarp();
+        if (MODE == 0) {
+#pragma unroll 1
+          for (int j = 0; j < NT / 4; ++j) {
+            const int v = NT > 32 && j >= 8 ? tok[(NT + 31) / 32 - 1] : tok[0];
+            const int l = (4 * j) & 31;
+            const int a0 = __shfl_sync(0xFFFFFFFFu, v, l), a1 = __shfl_sync(0xFFFFFFFFu, v, l + 1);
+            const int a2 = __shfl_sync(0xFFFFFFFFu, v, l + 2), a3 = __shfl_sync(0xFFFFFFFFu, v, l + 3);
+            if (elect_one())
+              fp8_tma_gather4(sw + W * WTILE + j * 4 * BK, &maps.a, &S->full[s], kb * BK, a0, a1, a2, a3);
+            __syncwarp();
+          }
+        }
+      }
+      // drain: wait (bounded) until every issued stage has landed
+      for (int j = i - STAGES < it ? it : i - STAGES; j < i; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
+    } else if (warp == 1) {   // -------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = fp8_idesc(128, NT);
+      const uint64_t desc0 = fp8_desc(smem_u32(base));
+      int i = it;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % STAGES, b = i % BUFS;
+        const bool ok = pipe_wait(&S->full[s], (i / STAGES) & 1, abort_flag, err, 127) &&
+                        pipe_wait(&S->tempty[b], ((i / BUFS) & 1) ^ 1, abort_flag, err, 127);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        fp8_fence_after();
+        if (elect_one()) {
+          const uint64_t dw = desc0 + (uint32_t)(s * (STAGE >> 4)), da = dw + (W * WTILE >> 4);
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              fp8_mma(tmem + b * COLS + w * NT, dw + w * (WTILE >> 4) + 2 * kk, da + 2 * kk, idesc, kk ? 1u : 0u);
+          fp8_commit(&S->done[s]);
+        }
+        __syncwarp();
+      }
+    } else if (warp < 4) {   // --------------------------------------------- factors
+      const int t = threadIdx.x - 64;
+      constexpr int OWN = (NT + 63) / 64;   // tokens of this thread: t, t + 64
+      const float* sa[OWN];
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        int q = row0 + min(t + 64 * i, valid - 1);
+        if (MODE == 0) q = e < 0 ? q - p.T * p.k : p.perm[q] / p.k;
+        sa[i] = p.a_scales + (long long)q * KB;
+      }
+      const float* sw[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        sw[w] = reinterpret_cast<const float*>(p.w_scales[w] + z * p.blob) + (long long)n * KB;
+      int c = ch;
+      for (int k0 = kb0; k0 < kb1; k0 += FK, ++c) {
+        const int b = c & 1;
+        float a[OWN][FK], w[W][FK];
+#pragma unroll
+        for (int j = 0; j < FK; ++j) {
+          const int kb = min(k0 + j, kb1 - 1);
+#pragma unroll
+          for (int i = 0; i < OWN; ++i) a[i][j] = sa[i][kb];
+#pragma unroll
+          for (int i = 0; i < W; ++i) w[i][j] = sw[i][kb];
+        }
+        if (!pipe_wait(&S->fempty[b], ((c >> 1) & 1) ^ 1, abort_flag, err, 129)) break;
+#pragma unroll
+        for (int j = 0; j < FK; ++j)
+#pragma unroll
+          for (int i = 0; i < OWN; ++i)
+            if (t + 64 * i < NT) {
+#pragma unroll
+              for (int x = 0; x < W; ++x) S->factor[b][j][x * NT + t + 64 * i] = a[i][j] * w[x][j];
+            }
+        mbar_arrive(&S->ffull[b]);
+      }
+    } else {   // ----------------------------------------------------------- sums
+      const int q = warp & 3, half = (warp - 4) >> 2;
+      const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+      constexpr int C1 = NT / C::SW, CHUNKS = COLS / C::SW / 16;   // columns per weight tile, 16-column chunks
+      float acc[CHUNKS * 16];
+#pragma unroll
+      for (int i = 0; i < CHUNKS * 16; ++i) acc[i] = 0.f;
+      auto column = [&](int j) { return (j / (C1 / 16)) * NT + half * C1 + (j % (C1 / 16)) * 16; };
+      int i = it, c = ch;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % STAGES, b = i % BUFS, f = (kb - kb0) % FK, fb = c & 1;
+        bool ok = true;
+        if (f == 0) ok = pipe_wait(&S->ffull[fb], (c >> 1) & 1, abort_flag, err, 128);
+        ok = ok && pipe_wait(&S->done[s], (i / STAGES) & 1, abort_flag, err, 128);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        fp8_fence_after();
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + b * COLS + column(j), v);
+          float4 x[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4*>(&S->factor[fb][f][column(j) + 4 * y]);
+          tmem_wait();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            fma_col(acc[16 * j + 4 * y], v[4 * y], x[y].x);
+            fma_col(acc[16 * j + 4 * y + 1], v[4 * y + 1], x[y].y);
+            fma_col(acc[16 * j + 4 * y + 2], v[4 * y + 2], x[y].z);
+            fma_col(acc[16 * j + 4 * y + 3], v[4 * y + 3], x[y].w);
+          }
+        }
+        fp8_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S->tempty[b]);
+          if (f == FK - 1 || kb == kb1 - 1) mbar_arrive(&S->fempty[fb]);
+        }
+        c += f == FK - 1 || kb == kb1 - 1;
+      }
+      // Every block of this CTA has been multiplied: the ring's memory is free for the sums.
+#pragma unroll
+      for (int j = 0; j < CHUNKS; ++j)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) part[(column(j) + x) * 128 + q * 32 + lane] = acc[16 * j + x];
+    }
+    __syncwarp();
+    it += kb1 - kb0;
+    ch += (kb1 - kb0 + FK - 1) / FK;
+    if (split > 1) cluster_sync(); else __syncthreads();
+
+    // columns of this rank, added over the ranks
+    const int r = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
+    const int c0 = NT * rank / split, c1 = min(NT * (rank + 1) / split, valid);
+    const int col = n * 128 + r;
+    auto total = [&](int c) {
+      const uint32_t at = smem_u32(part + c * 128 + r);
+      if (split == 1) return part[c * 128 + r];
+      float v[8], sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (x < split) v[x] = ld_rank(at, x);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (x < split) sum += v[x];
+      return sum;
+    };
+    if (MODE == 1) {
+      if (warp >= 4) {
+        for (int c = c0 + half; c < c1; c += C::SW) {
+          const float v = total(c);
+          const long long at = (long long)(row0 + c) * p.ldo + col;
+          if (col < p.N) {
+            if (p.out_bf16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)bf16x2(v, 0.f);
+            else static_cast<float*>(p.out)[at] = v;
+          }
+        }
+      }
+    } else {
+      if (warp >= 4) {
+        for (int c = c0 + half; c < c1; c += C::SW) {
+          const float h = silu(total(c)) * total(NT + c);
+          float m = amax_nan(0.f, h);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = amax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          if (lane == 0) S->wmax[warp & 3][c] = m;
+          part[c * 128 + r] = h;   // only this thread reads this sum of this rank
+        }
+      }
+      __syncthreads();
+      if (warp >= 4) {
+        for (int c = c0 + half; c < c1; c += C::SW) {
+          float m = S->wmax[0][c];
+#pragma unroll
+          for (int x = 1; x < 4; ++x) m = amax_nan(m, S->wmax[x][c]);
+          const float sc = fp8_scale(m);
+          const long long row = row0 + c;
+          if (col < p.N)
+            static_cast<uint8_t*>(p.out)[row * p.N + col] = (uint8_t)e4m3x2(part[c * 128 + r] * (1.0f / sc), 0.f);
+          if (r == 0) p.out_scales[row * NB + n] = sc;
+        }
+      }
+    }
+    // the sums have been read, by the other ranks too; the ring is the TMA's again
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (split > 1) cluster_sync(); else __syncthreads();
+  }
+  fp8_fence_before();
+  __syncthreads();
+  fp8_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
+}
+
+template <int MODE, int NT>
+cudaError_t launch_nt(const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int split, int chunks,
+                      cudaStream_t s) {
+  using C = Cfg<MODE, NT>;
+  auto kernel = fp8_stream_kernel<MODE, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.N + 127) / 128 * split), groups.n, chunks);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, groups, p, split);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8Maps& maps, const GemmGroups& groups,
+                              const Fp8Gemm& p, cudaStream_t s) {
+  if (groups.n <= 0 || p.T <= 0 || p.N <= 0) return cudaSuccess;
+  if (mode == 0) {
+    switch (nt) {
+      case 16: return launch_nt<0, 16>(maps, groups, p, split, chunks, s);
+      case 32: return launch_nt<0, 32>(maps, groups, p, split, chunks, s);
+      default: return launch_nt<0, 64>(maps, groups, p, split, chunks, s);
+    }
+  }
+  switch (nt) {
+    case 16: return launch_nt<1, 16>(maps, groups, p, split, chunks, s);
+    case 32: return launch_nt<1, 32>(maps, groups, p, split, chunks, s);
+    case 64: return launch_nt<1, 64>(maps, groups, p, split, chunks, s);
+    default: return launch_nt<1, 128>(maps, groups, p, split, chunks, s);
+  }
+}
+
+}  // namespace ftk
