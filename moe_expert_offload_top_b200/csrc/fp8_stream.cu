@@ -32,11 +32,11 @@ namespace {
 constexpr int BK = kFp8Block, WTILE = 128 * BK;
 constexpr int FK = 4;             // blocks of K per chunk of factors
 constexpr int TMEM_COLS = 256;
-constexpr int MAX_STAGES = 8, MAX_BUFS = 8;
+constexpr int MAX_STAGES = 8;
 
 template <int COLS, int NT>
 struct Ctrl {
-  uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_BUFS], ffull[2], fempty[2];
+  uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_STAGES], ffull[2], fempty[2];
   uint32_t tmem_base;
   int abort;
   alignas(16) float factor[2][FK][COLS];
@@ -55,7 +55,9 @@ struct Cfg {
   static constexpr int LIMIT = (228 * 1024) / PER_SM - 1024;
   static constexpr int FIT = (LIMIT - 1024 - (int)sizeof(Ctrl<COLS, NT>)) / STAGE;
   static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
-  static constexpr int BUFS = TMEM_COLS / COLS < MAX_BUFS ? TMEM_COLS / COLS : MAX_BUFS;
+  // Not more buffers than stages: the sums follow the blocks by the phases of the stages'
+  // barriers, and may be behind by the number of buffers.
+  static constexpr int BUFS = TMEM_COLS / COLS < STAGES ? TMEM_COLS / COLS : STAGES;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(Ctrl<COLS, NT>);
   static_assert(STAGES * STAGE >= COLS * 128 * 4, "the sums of a tile wait in the ring's memory");
 };

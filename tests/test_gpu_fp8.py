@@ -213,7 +213,8 @@ def _scales(shape, gen):
 GEMM_SHAPES = [  # M, N, K
     (1, 1, 1), (1, 16, 16), (1, 129, 128), (2, 300, 127), (3, 64, 129), (1, 4096, 1024), (16, 512, 640), (17, 128, 256),
     (31, 2001, 1133), (33, 256, 4096), (64, 768, 2048), (65, 130, 384), (127, 384, 257), (128, 256, 512),
-    (129, 257, 1000), (200, 1000, 200), (300, 520, 136), (513, 1300, 900), (1024, 2048, 512)]
+    (129, 257, 1000), (16, 16384, 2048), (32, 16384, 4096),
+    (200, 1000, 200), (300, 520, 136), (513, 1300, 900), (1024, 2048, 512)]
 
 
 @pytest.mark.parametrize("bf16", [True, False])
