@@ -565,8 +565,8 @@ FT_API int ft_expert_ffn_decode_noalloc(const void* x, int T, int H, int I, int 
  *   be residual, or x when ldx == ldr.  weight: [H], x's type.  y (may be NULL): [T][H] contiguous, x's type.
  *   q (may be NULL, y not both): bytes, rows ldq apart; the bytes past H of a row are not
  *   written.  scales: [T][ceil(H / 128)] f32.  1 <= H <= 32768, any strides of at least H.
- *   eps >= 0.  Rows whose widths, strides and addresses allow 16-byte accesses (H, the strides
- *   multiples of 8) run faster. */
+ *   eps >= 0.  Rows whose widths and strides are multiples of 16, at 32-byte aligned addresses
+ *   (q: 16), run faster. */
 FT_API int ft_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* weight,
                           int x_is_bf16, int T, int H, float eps, void* residual_out, void* y, void* q, long long ldq,
                           float* scales, void* stream);

@@ -29,4 +29,11 @@ FT_DEVICE uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Eight words to a 32-byte aligned address.
+FT_DEVICE void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 }  // namespace ftk

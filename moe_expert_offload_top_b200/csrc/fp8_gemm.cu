@@ -56,12 +56,6 @@ struct Smem {
   float factor[2][FK][2][BM];   // sa * sw of a row: by half of the columns, or for gate and up
 };
 
-// Eight words to a 32-byte aligned address.
-FT_DEVICE void st_sector(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 // v[i] of lane l <-> v[l] of lane i.
 FT_DEVICE void transpose32(uint32_t (&v)[32], int lane) {
 #pragma unroll

@@ -10,9 +10,11 @@
 // bits are the stored r, y and q (q from the fp32 y, not from the stored one).
 //
 // A row belongs to `tpr` threads (whole warps), so a row's sum is a warp sum plus one exchange
-// through shared memory.  Aligned rows: a thread owns 8 consecutive columns per chunk (16-byte
-// loads), a scale block is 16 lanes.  Others: a warp owns two scale blocks per chunk, lane l
-// the columns l, l+32, .. of each, so that element loads and byte stores still coalesce.
+// through shared memory.  Aligned rows: a thread owns 16 consecutive columns per chunk (32-byte
+// loads), a scale block is 8 lanes; with 8 columns per thread the two divisions and the
+// maximum's exchange, the same work per thread, kept the issue slots half busy.  Others: a warp
+// owns four scale blocks per chunk, lane l the columns l, l+32, .. of each, so that element
+// loads and byte stores still coalesce.
 #include "fp8.hpp"
 #include "fp8_common.cuh"
 
@@ -28,33 +30,48 @@ FT_DEVICE void store1(void* p, long long i, float v, bool bf16) {
   else
     static_cast<float*>(p)[i] = v;
 }
+FT_DEVICE void ld_sector(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p) : "memory");
+}
+// 16 consecutive elements, 32-byte aligned.
 template <bool BF16>
-FT_DEVICE void load8(const void* p, long long i, float* v) {
+FT_DEVICE void load16(const void* p, long long i, float* v) {
+  uint32_t w[8];
   if constexpr (BF16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    ld_sector(static_cast<const uint16_t*>(p) + i, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) { v[2 * j] = bf16lo(w[j]); v[2 * j + 1] = bf16hi(w[j]); }
+    for (int j = 0; j < 8; ++j) { v[2 * j] = bf16lo(w[j]); v[2 * j + 1] = bf16hi(w[j]); }
   } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ld_sector(static_cast<const float*>(p) + i + 8 * h, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * h + j] = __uint_as_float(w[j]);
+    }
   }
 }
 template <bool BF16>
-FT_DEVICE void store8(void* p, long long i, const float* v) {
+FT_DEVICE void store16(void* p, long long i, const float* v) {
+  uint32_t w[8];
   if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+    st_sector(static_cast<uint16_t*>(p) + i, w);
   } else {
-    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    f[0] = make_float4(v[0], v[1], v[2], v[3]);
-    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * h + j]);
+      st_sector(static_cast<float*>(p) + i + 8 * h, w);
+    }
   }
 }
+constexpr int E = 16;         // elements of a thread per chunk
+constexpr int UNIT = 32 * E;  // columns of a warp per chunk
 
-// blockDim = (tpr, rows per block).  CH: chunks of 8 elements a thread holds.
+// blockDim = (tpr, rows per block).  CH: chunks a thread holds.
 template <bool BF16, bool NORM, bool VEC, int CH>
 __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ RowsFp8 p) {
   __shared__ float part[32];
@@ -66,43 +83,41 @@ __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ 
 
   // column of element i of chunk c
   auto col = [&](int c, int i) {
-    if constexpr (VEC) return (c * tpr + t) * 8 + i;
-    return ((c * warps + warp) * 2 + (i >> 2)) * kFp8Block + (i & 3) * 32 + lane;
+    if constexpr (VEC) return (c * tpr + t) * E + i;
+    return ((c * warps + warp) * (E / 4) + (i >> 2)) * kFp8Block + (i & 3) * 32 + lane;
   };
-  float v[CH][8];
+  float v[CH][E];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
-    if (!live) continue;
+    for (int i = 0; i < E; ++i) v[c][i] = 0.f;
     if constexpr (VEC) {
-      if (col(c, 0) < H) load8<BF16>(p.x, row * p.ldx + col(c, 0), v[c]);
+      if (live && col(c, 0) < H) {
+        load16<BF16>(p.x, row * p.ldx + col(c, 0), v[c]);
+        if (NORM && p.residual) {
+          float r[E];
+          load16<BF16>(p.residual, row * p.ldr + col(c, 0), r);
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[c][i] += r[i];
+        }
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col(c, i) < H) v[c][i] = load1(p.x, row * p.ldx + col(c, i), BF16);
+      for (int i = 0; i < E; ++i)
+        if (live && col(c, i) < H) {
+          v[c][i] = load1(p.x, row * p.ldx + col(c, i), BF16);
+          if (NORM && p.residual) v[c][i] += load1(p.residual, row * p.ldr + col(c, i), BF16);
+        }
     }
   }
   if constexpr (NORM) {
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (live && p.residual) {
-        if constexpr (VEC) {
-          if (col(c, 0) < H) {
-            float r[8];
-            load8<BF16>(p.residual, row * p.ldr + col(c, 0), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] += r[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col(c, i) < H) v[c][i] += load1(p.residual, row * p.ldr + col(c, i), BF16);
-        }
+      if (p.residual) {
         if constexpr (BF16) {   // the norm is that of the stored stream
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
+          for (int i = 0; i < E; i += 2) {
             const uint32_t w = bf16x2(v[c][i], v[c][i + 1]);
             v[c][i] = bf16lo(w);
             v[c][i + 1] = bf16hi(w);
@@ -111,15 +126,15 @@ __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ 
       }
       if (live && p.residual_out) {
         if constexpr (VEC) {
-          if (col(c, 0) < H) store8<BF16>(p.residual_out, row * p.ldr + col(c, 0), v[c]);
+          if (col(c, 0) < H) store16<BF16>(p.residual_out, row * p.ldr + col(c, 0), v[c]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < E; ++i)
             if (col(c, i) < H) store1(p.residual_out, row * p.ldr + col(c, i), v[c][i], BF16);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i], v[c][i], sum);
+      for (int i = 0; i < E; ++i) sum = fmaf(v[c][i], v[c][i], sum);
     }
     sum = warp_sum(sum);
     if (warps > 1) {
@@ -134,15 +149,15 @@ __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ 
     for (int c = 0; c < CH; ++c) {
       if constexpr (VEC) {
         if (col(c, 0) < H) {
-          float w[8];
-          load8<BF16>(p.weight, col(c, 0), w);
+          float w[E];
+          load16<BF16>(p.weight, col(c, 0), w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * inv * w[i];
-          if (live && p.y) store8<BF16>(p.y, row * H + col(c, 0), v[c]);
+          for (int i = 0; i < E; ++i) v[c][i] = v[c][i] * inv * w[i];
+          if (live && p.y) store16<BF16>(p.y, row * H + col(c, 0), v[c]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < E; ++i)
           if (col(c, i) < H) {
             v[c][i] = v[c][i] * inv * load1(p.weight, col(c, i), BF16);
             if (live && p.y) store1(p.y, row * H + col(c, i), v[c][i], BF16);
@@ -157,20 +172,23 @@ __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ 
     if constexpr (VEC) {
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = amax_nan(m, v[c][i]);
+      for (int i = 0; i < E; ++i) m = amax_nan(m, v[c][i]);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = amax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      for (int o = 4; o > 0; o >>= 1) m = amax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       const float s = fp8_scale(m), inv = 1.0f / s;
       if (live && col(c, 0) < H) {
-        uint2 w;
-        w.x = e4m3x2(v[c][0] * inv, v[c][1] * inv) | e4m3x2(v[c][2] * inv, v[c][3] * inv) << 16;
-        w.y = e4m3x2(v[c][4] * inv, v[c][5] * inv) | e4m3x2(v[c][6] * inv, v[c][7] * inv) << 16;
-        *reinterpret_cast<uint2*>(p.q + row * p.ldq + col(c, 0)) = w;
-        if ((lane & 15) == 0) p.scales[row * blocks + col(c, 0) / kFp8Block] = s;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* x = v[c] + 4 * i;
+          w[i] = e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16;
+        }
+        *reinterpret_cast<uint4*>(p.q + row * p.ldq + col(c, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+        if ((lane & 7) == 0) p.scales[row * blocks + col(c, 0) / kFp8Block] = s;
       }
     } else {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < E / 4; ++b) {
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = amax_nan(m, v[c][4 * b + i]);
@@ -190,11 +208,10 @@ __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ 
 
 template <bool BF16, bool NORM, bool VEC>
 cudaError_t launch_rows(const RowsFp8& p, int ch, dim3 grid, dim3 block, cudaStream_t s) {
-  switch (ch) {
-    case 1: rows_fp8_kernel<BF16, NORM, VEC, 1><<<grid, block, 0, s>>>(p); break;
-    case 2: rows_fp8_kernel<BF16, NORM, VEC, 2><<<grid, block, 0, s>>>(p); break;
-    default: rows_fp8_kernel<BF16, NORM, VEC, 4><<<grid, block, 0, s>>>(p); break;
-  }
+  if (ch == 1)
+    rows_fp8_kernel<BF16, NORM, VEC, 1><<<grid, block, 0, s>>>(p);
+  else
+    rows_fp8_kernel<BF16, NORM, VEC, 2><<<grid, block, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <bool BF16, bool NORM>
@@ -208,18 +225,12 @@ cudaError_t launch_rows(const RowsFp8& p, bool vec, int ch, dim3 grid, dim3 bloc
 cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, cudaStream_t s) {
   if (p.T <= 0) return cudaSuccess;
   auto aligned = [](const void* q, int bytes) { return ((uintptr_t)q & (bytes - 1)) == 0; };
-  const bool vec = p.H % 8 == 0 && p.ldx % 8 == 0 && aligned(p.x, 16) &&
-                   ((!p.residual && !p.residual_out) || p.ldr % 8 == 0) && aligned(p.residual, 16) &&
-                   aligned(p.residual_out, 16) && aligned(p.weight, 16) && aligned(p.y, 16) &&
-                   (!p.q || (p.ldq % 8 == 0 && aligned(p.q, 8)));
-  // units of 256 columns (a warp's chunk); a warp takes ch of them
-  const int units = (p.H + 255) / 256;
-  // Few rows: one chunk per thread, the shortest chain from load to store.  Many rows: up to
-  // four chunks in flight per thread and several rows per SM.
-  const int few = p.T <= 2 * 148 ? 32 : 8;
-  int ch = 1;
-  while (ch < 4 && (units + ch - 1) / ch > few) ch *= 2;
-  const int warps = (units + ch - 1) / ch;
+  const bool vec = p.H % E == 0 && p.ldx % E == 0 && aligned(p.x, 32) &&
+                   ((!p.residual && !p.residual_out) || p.ldr % E == 0) && aligned(p.residual, 32) &&
+                   aligned(p.residual_out, 32) && aligned(p.weight, 32) && aligned(p.y, 32) &&
+                   (!p.q || (p.ldq % 16 == 0 && aligned(p.q, 16)));
+  // one chunk per thread while a block can hold the row's threads: the shortest way from load to store
+  const int units = (p.H + UNIT - 1) / UNIT, ch = units <= 32 ? 1 : 2, warps = (units + ch - 1) / ch;
   const int rows = warps >= 4 ? 1 : 4 / warps;
   const dim3 block(warps * 32, rows), grid((unsigned)(((long long)p.T + rows - 1) / rows));
   if (p.weight)
