@@ -61,9 +61,10 @@ cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& gro
 // The same product with the weights as the tensor cores' M, for few rows (fp8_stream.cu): nt
 // tokens (16, 32, 64; mode 1: 128) per CTA, K split over clusters of `split` CTAs (1 .. 8, at most
 // the blocks of K), `chunks` CTAs sharing a group's token chunks.  maps.a: mode 0 boxes of one
-// row of x, mode 1 of nt rows.
+// row of x, mode 1 of nt rows.  after_gate_up: this launch directly follows the gate/up launch
+// (mode 0 of this kernel) that writes its rows, and loads weights while that one finishes.
 cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8Maps& maps, const GemmGroups& groups,
-                              const Fp8Gemm& p, cudaStream_t s);
+                              const Fp8Gemm& p, bool after_gate_up, cudaStream_t s);
 // dst + q * stride = the H bytes of pair q's token row, for the pairs of the groups.
 cudaError_t launch_fp8_gather(const void* x, long long ldx, const GemmGroups& groups, const int* offsets,
                               const int* perm, int T, int k, int H, void* dst, long long stride, int num_sms,

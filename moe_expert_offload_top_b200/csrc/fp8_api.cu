@@ -57,7 +57,7 @@ Plan plan(int mode, long long rows, int groups, int N, int K, int sms) {
   pl.chunks = (int)((rows + pl.nt - 1) / pl.nt);
   const long long tiles = (long long)ftk::fp8_blocks(N) * groups * pl.chunks;
   const int kb = ftk::fp8_blocks(K);
-  while (pl.split < 8 && tiles * pl.split < 2 * sms && kb >= 4 * pl.split) pl.split *= 2;
+  while (pl.split < 8 && 3 * tiles * pl.split < 2 * sms && kb >= 4 * pl.split) pl.split *= 2;
   return pl;
 }
 
@@ -129,7 +129,7 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(w_scales);
   const ftk::Fp8Gemm p{a_scales, {ws, ws}, 0, nullptr, nullptr, M, 0, N, K, out, nullptr, ldo, out_is_bf16 != 0, err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = pl.nt ? ftk::launch_fp8_stream(1, pl.nt, pl.split, pl.chunks, m, groups, p, s)
+  const cudaError_t e = pl.nt ? ftk::launch_fp8_stream(1, pl.nt, pl.split, pl.chunks, m, groups, p, false, s)
                               : ftk::launch_fp8_gemm(1, m, groups, p, sms, s);
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
@@ -195,14 +195,14 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (pu.nt) {
-    e = ftk::launch_fp8_stream(0, pu.nt, pu.split, pu.chunks, up, groups, g, s);
+    e = ftk::launch_fp8_stream(0, pu.nt, pu.split, pu.chunks, up, groups, g, false, s);
   } else {
     // the pairs' token rows wait in the rows of y that the down product writes last
     e = ftk::launch_fp8_gather(x, ldx, groups, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
     if (e == cudaSuccess) e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
   }
   if (e == cudaSuccess)
-    e = pd.nt ? ftk::launch_fp8_stream(1, pd.nt, pd.split, pd.chunks, down, groups, d, s)
+    e = pd.nt ? ftk::launch_fp8_stream(1, pd.nt, pd.split, pd.chunks, down, groups, d, pu.nt > 0, s)
               : ftk::launch_fp8_gemm(1, down, groups, d, sms, s);
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }

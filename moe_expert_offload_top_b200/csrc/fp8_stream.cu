@@ -99,25 +99,39 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
   const int n = blockIdx.x / split, g = blockIdx.y;
   const int kb0 = (int)((long long)KB * rank / split), kb1 = (int)((long long)KB * (rank + 1) / split);
   const int e = groups.expert[g], z = groups.z[g];
+  int* err = p.err;
+  // the same for every CTA of a cluster (they differ in blockIdx.x only)
   const int first = e >= 0 ? p.offsets[e] : p.T * p.k;
   const int rows = e >= 0 ? p.offsets[e + 1] - first : p.T;
-  // the same for every CTA of a cluster (they differ in blockIdx.x only)
-  if ((long long)blockIdx.z * NT >= rows) return;
-  int* err = p.err;
+  const bool some = (long long)blockIdx.z * NT < rows;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&S->full[s], 1);
-      mbar_init(&S->done[s], 1);
+  auto load_weights = [&](int s, int kb) {   // one thread: the stage's barrier and weight tiles
+    unsigned char* sw = base + s * STAGE;
+    mbar_expect_tx(&S->full[s], STAGE);
+    fp8_tma_3d(sw, &maps.b[0], &S->full[s], kb * BK, n * 128, z);
+    if (W == 2) fp8_tma_3d(sw + WTILE, &maps.b[1], &S->full[s], kb * BK, n * 128, z);
+  };
+  // The first weights are on their way before the CTA is set up, and before the kernel that
+  // writes the tokens has finished (griddepcontrol below): they depend on neither.
+  const int ahead = min(STAGES, kb1 - kb0);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(&S->full[s], 1);
+        mbar_init(&S->done[s], 1);
+      }
+      for (int b = 0; b < BUFS; ++b) mbar_init(&S->tempty[b], 4 * C::SW);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&S->ffull[b], 64);
+        mbar_init(&S->fempty[b], 4 * C::SW);
+      }
+      S->abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (some)
+        for (int j = 0; j < ahead; ++j) load_weights(j, kb0 + j);
     }
-    for (int b = 0; b < BUFS; ++b) mbar_init(&S->tempty[b], 4 * C::SW);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&S->ffull[b], 64);
-      mbar_init(&S->fempty[b], 4 * C::SW);
-    }
-    S->abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -129,6 +143,10 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
   fp8_fence_after();
   const uint32_t tmem = S->tmem_base;
   volatile int* abort_flag = &S->abort;
+  // gate/up: every CTA is running, so the down product may start to load its weights; down: the
+  // rows and scales of h (and what else the launches before it wrote) are complete after the wait.
+  if (MODE == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else asm volatile("griddepcontrol.wait;" ::: "memory");
 
   int it = 0, ch = 0;   // blocks of K and chunks of factors so far
   for (int t0 = blockIdx.z * NT; t0 < rows; t0 += gridDim.z * NT) {
@@ -148,9 +166,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         if (!__all_sync(0xFFFFFFFFu, pipe_wait(&S->done[s], ((i / STAGES) & 1) ^ 1, abort_flag, err, 126))) break;
         unsigned char* sw = base + s * STAGE;
         if (elect_one()) {
-          mbar_expect_tx(&S->full[s], STAGE);
-          fp8_tma_3d(sw, &maps.b[0], &S->full[s], kb * BK, n * 128, z);
-          if (W == 2) fp8_tma_3d(sw + WTILE, &maps.b[1], &S->full[s], kb * BK, n * 128, z);
+          if (i >= ahead) load_weights(s, kb);
           if (MODE == 1) fp8_tma_2d(sw + W * WTILE, &maps.a, &S->full[s], kb * BK, row0);
         }
         __syncwarp();
@@ -343,12 +359,12 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
 
 template <int MODE, int NT>
 cudaError_t launch_nt(const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int split, int chunks,
-                      cudaStream_t s) {
+                      bool after_gate_up, cudaStream_t s) {
   using C = Cfg<MODE, NT>;
   auto kernel = fp8_stream_kernel<MODE, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -359,26 +375,31 @@ cudaError_t launch_nt(const Fp8Maps& maps, const GemmGroups& groups, const Fp8Ge
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if (after_gate_up) {   // may start while the gate/up kernel finishes (griddepcontrol)
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, maps, groups, p, split);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8Maps& maps, const GemmGroups& groups,
-                              const Fp8Gemm& p, cudaStream_t s) {
+                              const Fp8Gemm& p, bool after_gate_up, cudaStream_t s) {
   if (groups.n <= 0 || p.T <= 0 || p.N <= 0) return cudaSuccess;
   if (mode == 0) {
     switch (nt) {
-      case 16: return launch_nt<0, 16>(maps, groups, p, split, chunks, s);
-      case 32: return launch_nt<0, 32>(maps, groups, p, split, chunks, s);
-      default: return launch_nt<0, 64>(maps, groups, p, split, chunks, s);
+      case 16: return launch_nt<0, 16>(maps, groups, p, split, chunks, after_gate_up, s);
+      case 32: return launch_nt<0, 32>(maps, groups, p, split, chunks, after_gate_up, s);
+      default: return launch_nt<0, 64>(maps, groups, p, split, chunks, after_gate_up, s);
     }
   }
   switch (nt) {
-    case 16: return launch_nt<1, 16>(maps, groups, p, split, chunks, s);
-    case 32: return launch_nt<1, 32>(maps, groups, p, split, chunks, s);
-    case 64: return launch_nt<1, 64>(maps, groups, p, split, chunks, s);
-    default: return launch_nt<1, 128>(maps, groups, p, split, chunks, s);
+    case 16: return launch_nt<1, 16>(maps, groups, p, split, chunks, after_gate_up, s);
+    case 32: return launch_nt<1, 32>(maps, groups, p, split, chunks, after_gate_up, s);
+    case 64: return launch_nt<1, 64>(maps, groups, p, split, chunks, after_gate_up, s);
+    default: return launch_nt<1, 128>(maps, groups, p, split, chunks, after_gate_up, s);
   }
 }
 
