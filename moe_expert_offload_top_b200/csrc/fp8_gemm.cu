@@ -39,11 +39,22 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = kFp8Block;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4, TMEM_COLS = 512;
-constexpr int SUM_WARPS = 8, THREADS = 128 + 32 * SUM_WARPS;
+#ifndef SW_
+#define SW_ 8
+#endif
+constexpr int SUM_WARPS = SW_, THREADS = 128 + 32 * SUM_WARPS;
+constexpr int GROUPS = SUM_WARPS / 4;         // warpgroups that share a tile's columns
+constexpr int GC = BN / GROUPS;               // columns of a summing thread
+constexpr int LC = GROUPS == 2 ? 32 : 16;     // columns of a TMEM load
 constexpr int FK = 8;   // blocks of K per chunk of factors
 // registers: (4 * 72 + 8 * 216) * 32 = 384 * 168, the launch's
+#if SW_ == 8
 #define FP8_GEMM_CONTROL_REGS 72
 #define FP8_GEMM_SUM_REGS 216
+#else
+#define FP8_GEMM_CONTROL_REGS 56
+#define FP8_GEMM_SUM_REGS 104
+#endif
 
 struct Smem {
   uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves;
@@ -52,7 +63,7 @@ struct Smem {
   int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
   int row_start[kMaxList];
   int rows[kMaxList];
-  float amax[2][2][BM];         // gate/up: a row's largest |h| per half, double-buffered by tile
+  float amax[2][GROUPS][BM];    // gate/up: a row's largest |h| per warpgroup, double-buffered by tile
   float factor[2][FK][2][BM];   // sa * sw of a row: by half of the columns, or for gate and up
 };
 
@@ -97,10 +108,10 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S->tempty[b], SUM_WARPS);
-      mbar_init(&S->ffull[b], 64);
+      mbar_init(&S->ffull[b], 2);
       mbar_init(&S->fempty[b], SUM_WARPS);
     }
-    mbar_init(&S->halves, 32 * SUM_WARPS);
+    mbar_init(&S->halves, SUM_WARPS);
     S->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -158,7 +169,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       bool stop = false;
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int s = it % STAGES;
-        if (!__all_sync(0xFFFFFFFFu, pipe_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121))) {
+        if (!warp_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121)) {
           stop = true;
           break;
         }
@@ -175,28 +186,25 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       if (stop) break;
     }
     // drain: wait (bounded) until every issued stage has landed
-    for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
+    if (lane == 0)
+      for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
   } else if (warp == 1) {   // ------------------------------------------- MMA issuer
     constexpr uint32_t idesc = fp8_idesc(BM, BN);
     const uint64_t desc0 = fp8_desc(smem_u32(base));   // stage s, K step kk: + (s * STAGE_BYTES + kk * 32) / 16
+    // a block starts its sums afresh: the issuer sees blocks, not tiles
+    const long long mine = total_tiles > blockIdx.x ? (total_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
     int it = 0;
-    bool ok = true;
-    for (long long t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int s = it % STAGES, b = it & 1;
-        ok = pipe_wait(&S->full[s], (it / STAGES) & 1, abort_flag, err, 122) &&
-             pipe_wait(&S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        fp8_fence_after();
-        if (elect_one()) {
-          const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
+    for (long long left = mine * KB; left > 0; --left, ++it) {
+      const int s = it % STAGES, b = it & 1;
+      if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122)) break;
+      fp8_fence_after();
+      if (elect_one()) {
+        const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk) fp8_mma(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
-          fp8_commit(&S->done[s]);   // frees the stage and hands the buffer to the sums
-        }
-        __syncwarp();
+        for (int kk = 0; kk < BK / 32; ++kk) fp8_mma(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+        fp8_commit(&S->done[s]);   // frees the stage and hands the buffer to the sums
       }
+      __syncwarp();
     }
   } else {   // ---------------------------------------------------------- factors
     const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
@@ -230,7 +238,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
             w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
             a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
           }
-        ok = pipe_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
+        ok = warp_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < FK; ++j)
@@ -239,95 +247,95 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
             S->factor[b][j][0][r0 + 64 * i] = a[i][j] * w[0][j];
             S->factor[b][j][1][r0 + 64 * i] = a[i][j] * w[1][j];
           }
-        mbar_arrive(&S->ffull[b]);
+        warp_arrive(&S->ffull[b]);
       }
       if (!ok) break;
     }
   }
   } else {   // -------------------------------------------------------- sums and output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8_GEMM_SUM_REGS));
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int q = warp & 3, grp = (warp - 4) >> 2;
     const int r = q * 32 + lane;               // tile row of this thread
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const int NB = (p.N + kFp8Block - 1) / kFp8Block;
-    // half h sums columns 128 h .. of a product tile; columns 64 h .. of gate and of up
-    const uint32_t col0 = lane_base + half * (MODE == 0 ? 64 : BN / 2);
-    constexpr uint32_t HOP = MODE == 0 ? BN / 2 : 64;   // from the first 64 of its columns to the other 64
+    // warpgroup g sums columns GC g .. of a product tile; columns GC/2 g .. of gate and of up
+    constexpr int NL = GC / LC;   // TMEM loads per block
+    const uint32_t col0 = lane_base + grp * (MODE == 0 ? GC / 2 : GC);
+    auto column = [&](int c) {
+      return MODE == 0 ? (c / (NL / 2)) * (BN / 2) + (c % (NL / 2)) * LC : c * LC;
+    };
+    const int half = grp * 2 / GROUPS;   // the factor of a product tile's column
     int it = 0, tl = 0, ch = 0;
     for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
       int g, m, n;
       decode(t, g, m, n);
       const bool valid = r < S->rows[g] - m * BM;
       const long long row = S->row_start[g] + (long long)m * BM + r;
-      float acc[128];
+      float acc[GC];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < GC; ++i) acc[i] = 0.f;
       // The next block's first columns are asked for before this one's last are added, so that
       // the wait for the tensor cores and the load's latency pass behind multiply-adds.
-      uint32_t v0[32], v1[32];
+      uint32_t v[2][LC];
       auto ready = [&](int i) {   // accumulators of block i (over the tiles)
-        const bool w = pipe_wait(&S->done[i % STAGES], (i / STAGES) & 1, abort_flag, err, 123);
-        const bool all = __all_sync(0xFFFFFFFFu, w);
+        const bool w = warp_wait(&S->done[i % STAGES], (i / STAGES) & 1, abort_flag, err, 123);
         fp8_fence_after();
-        return all;
+        return w;
       };
       bool ok = ready(it);
       if (!ok) break;
-      tmem_ld32(col0 + (it & 1) * BN, v0);
+      tmem_ld(col0 + (it & 1) * BN, v[0]);
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int b = it & 1, j = kb % FK, fb = ch & 1;
         if (j == 0) {
-          ok = __all_sync(0xFFFFFFFFu, pipe_wait(&S->ffull[fb], (ch >> 1) & 1, abort_flag, err, 123));
+          ok = warp_wait(&S->ffull[fb], (ch >> 1) & 1, abort_flag, err, 123);
           if (!ok) break;
         }
         const uint32_t ta = col0 + b * BN;
         const float f0 = S->factor[fb][j][MODE == 0 ? 0 : half][r], f1 = MODE == 0 ? S->factor[fb][j][1][r] : f0;
-        tmem_wait();
-        tmem_ld32(ta + 32, v1);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) fma_col(acc[i], v0[i], f0);
-        tmem_wait();
-        tmem_ld32(ta + HOP, v0);
+        for (int c = 0; c < NL; ++c) {
+          tmem_wait();
+          if (c + 1 < NL) {
+            tmem_ld(ta + column(c + 1), v[(c + 1) & 1]);
+          } else {
+            fp8_fence_before();
+            warp_arrive(&S->tempty[b]);   // every lane's values are in registers
+            const bool chunk_done = j == FK - 1 || kb == KB - 1;
+            if (chunk_done) warp_arrive(&S->fempty[fb]);
+            ch += chunk_done;
+            if (kb + 1 < KB) {
+              ok = ready(it + 1);
+              if (!ok) break;
+              tmem_ld(col0 + (b ^ 1) * BN, v[0]);
+            }
+          }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) fma_col(acc[32 + i], v1[i], f0);
-        tmem_wait();
-        tmem_ld32(ta + HOP + 32, v1);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) fma_col(acc[64 + i], v0[i], f1);
-        tmem_wait();
-        fp8_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S->tempty[b]);   // every lane's values are in registers
-        const bool chunk_done = j == FK - 1 || kb == KB - 1;
-        if (chunk_done && lane == 0) mbar_arrive(&S->fempty[fb]);
-        ch += chunk_done;
-        if (kb + 1 < KB) {
-          ok = ready(it + 1);
-          if (!ok) break;
-          tmem_ld32(col0 + (b ^ 1) * BN, v0);
+          for (int i = 0; i < LC; ++i) fma_col(acc[LC * c + i], v[c & 1][i], MODE == 0 && c >= NL / 2 ? f1 : f0);
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) fma_col(acc[96 + i], v1[i], f1);
+        if (!ok) break;
       }
       if (!ok) break;
       if (MODE == 0) {
-        float h[64], mx = 0.f;
+        constexpr int HC = GC / 2;
+        float h[HC], mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          h[i] = silu(acc[i]) * acc[64 + i];
+        for (int i = 0; i < HC; ++i) {
+          h[i] = silu(acc[i]) * acc[HC + i];
           mx = amax_nan(mx, h[i]);
         }
-        S->amax[tl & 1][half][r] = mx;
-        mbar_arrive(&S->halves);
-        ok = __all_sync(0xFFFFFFFFu, pipe_wait(&S->halves, tl & 1, abort_flag, err, 124));
+        S->amax[tl & 1][grp][r] = mx;
+        warp_arrive(&S->halves);
+        ok = warp_wait(&S->halves, tl & 1, abort_flag, err, 124);
         if (!ok) break;
-        mx = amax_nan(mx, S->amax[tl & 1][half ^ 1][r]);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) mx = amax_nan(mx, S->amax[tl & 1][i][r]);
         const float sc = fp8_scale(mx), inv = 1.0f / sc;
         if (valid) {
-          const int c0 = n * TN + half * 64;
+          const int c0 = n * TN + grp * HC;
           uint8_t* dst = static_cast<uint8_t*>(p.out) + row * p.N + c0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < HC / 16; ++j)
             if (c0 + 16 * j < p.N) {   // N is a multiple of 16
               uint32_t w[4];
 #pragma unroll
@@ -337,18 +345,18 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               }
               *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          if (half == 0) p.out_scales[row * NB + n] = sc;
+          if (grp == 0) p.out_scales[row * NB + n] = sc;
         }
       } else {
-        const int c0 = n * TN + half * (BN / 2);
+        const int c0 = n * TN + grp * GC;
         const int es = p.out_bf16 ? 2 : 4;
         unsigned char* dst = static_cast<unsigned char*>(p.out) + (row * p.ldo + c0) * es;
-        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + BN / 2 <= p.N) {
+        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + GC <= p.N) {
           // a thread stores its own row, a whole 32-byte sector at a time
           if (valid) {
             if (p.out_bf16) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
+              for (int j = 0; j < GC / 16; ++j) {
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = bf16x2(acc[16 * j + 2 * i], acc[16 * j + 2 * i + 1]);
@@ -356,7 +364,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               }
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < GC / 8; ++j) {
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[8 * j + i]);
@@ -369,7 +377,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
           // consecutive columns of a row
           const int rows_left = S->rows[g] - m * BM - q * 32;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < GC / 32; ++j) {
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);

@@ -29,11 +29,25 @@ FT_DEVICE void fp8_tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
       : "memory");
 }
 
-// mbar_wait for the pipelines below: the clock is read only once a wait has lasted a while.
-FT_DEVICE bool pipe_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err, int code) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try(b, parity)) return true;
-  return mbar_wait(b, parity, abort_flag, err, code);
+// mbar_wait by a converged warp, which stays one; true when every lane's wait succeeded.  The
+// first try is apart from the loop: a phase that is over costs 75 cycles so (a loop around the
+// try, even one left at once, 290).
+FT_DEVICE bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try(b, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(b, parity, abort_flag, err, code));
+}
+// Both phases over: the two first tries overlap.
+FT_DEVICE bool warp_wait2(uint64_t* b0, uint32_t parity0, uint64_t* b1, uint32_t parity1, volatile int* abort_flag,
+                          int* err, int code) {
+  const bool t0 = mbar_try(b0, parity0), t1 = mbar_try(b1, parity1);
+  if (__all_sync(0xFFFFFFFFu, t0 && t1)) return true;
+  const bool ok = mbar_wait(b0, parity0, abort_flag, err, code) && mbar_wait(b1, parity1, abort_flag, err, code);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+// One arrival for the warp, behind everything its lanes did before.
+FT_DEVICE void warp_arrive(uint64_t* b) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(b);
 }
 
 // One lane of a converged warp.  The compiler then knows that what follows runs in one thread,
@@ -67,8 +81,16 @@ FT_DEVICE void fp8_commit(uint64_t* bar) {
 FT_DEVICE void fp8_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 FT_DEVICE void fp8_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 accumulator columns of this thread's TMEM lane; tmem_wait before the values are used.
-FT_DEVICE void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 or 32 accumulator columns of this thread's TMEM lane; tmem_wait before the values are used.
+FT_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+FT_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"

@@ -62,14 +62,6 @@ struct Cfg {
   static_assert(STAGES * STAGE >= COLS * 128 * 4, "the sums of a tile wait in the ring's memory");
 };
 
-FT_DEVICE void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 FT_DEVICE void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -122,7 +114,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
       }
       for (int b = 0; b < BUFS; ++b) mbar_init(&S->tempty[b], 4 * C::SW);
       for (int b = 0; b < 2; ++b) {
-        mbar_init(&S->ffull[b], 64);
+        mbar_init(&S->ffull[b], 2);
         mbar_init(&S->fempty[b], 4 * C::SW);
       }
       S->abort = 0;
@@ -163,7 +155,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
       int i = it;
       for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int s = i % STAGES;
-        if (!__all_sync(0xFFFFFFFFu, pipe_wait(&S->done[s], ((i / STAGES) & 1) ^ 1, abort_flag, err, 126))) break;
+        if (!warp_wait(&S->done[s], ((i / STAGES) & 1) ^ 1, abort_flag, err, 126)) break;
         unsigned char* sw = base + s * STAGE;
         if (elect_one()) {
           if (i >= ahead) load_weights(s, kb);
@@ -184,16 +176,16 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         }
       }
       // drain: wait (bounded) until every issued stage has landed
-      for (int j = i - STAGES < it ? it : i - STAGES; j < i; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
+      if (lane == 0)
+        for (int j = i - STAGES < it ? it : i - STAGES; j < i; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
     } else if (warp == 1) {   // -------------------------------------------- MMA issuer
       constexpr uint32_t idesc = fp8_idesc(128, NT);
       const uint64_t desc0 = fp8_desc(smem_u32(base));
       int i = it;
       for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int s = i % STAGES, b = i % BUFS;
-        const bool ok = pipe_wait(&S->full[s], (i / STAGES) & 1, abort_flag, err, 127) &&
-                        pipe_wait(&S->tempty[b], ((i / BUFS) & 1) ^ 1, abort_flag, err, 127);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (!warp_wait2(&S->full[s], (i / STAGES) & 1, &S->tempty[b], ((i / BUFS) & 1) ^ 1, abort_flag, err, 127))
+          break;
         fp8_fence_after();
         if (elect_one()) {
           const uint64_t dw = desc0 + (uint32_t)(s * (STAGE >> 4)), da = dw + (W * WTILE >> 4);
@@ -232,7 +224,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < W; ++i) w[i][j] = sw[i][kb];
         }
-        if (!pipe_wait(&S->fempty[b], ((c >> 1) & 1) ^ 1, abort_flag, err, 129)) break;
+        if (!warp_wait(&S->fempty[b], ((c >> 1) & 1) ^ 1, abort_flag, err, 129)) break;
 #pragma unroll
         for (int j = 0; j < FK; ++j)
 #pragma unroll
@@ -241,7 +233,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
 #pragma unroll
               for (int x = 0; x < W; ++x) S->factor[b][j][x * NT + t + 64 * i] = a[i][j] * w[x][j];
             }
-        mbar_arrive(&S->ffull[b]);
+        warp_arrive(&S->ffull[b]);
       }
     } else {   // ----------------------------------------------------------- sums
       const int q = warp & 3, half = (warp - 4) >> 2;
@@ -255,14 +247,14 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
       for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int s = i % STAGES, b = i % BUFS, f = (kb - kb0) % FK, fb = c & 1;
         bool ok = true;
-        if (f == 0) ok = pipe_wait(&S->ffull[fb], (c >> 1) & 1, abort_flag, err, 128);
-        ok = ok && pipe_wait(&S->done[s], (i / STAGES) & 1, abort_flag, err, 128);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (f == 0) ok = warp_wait(&S->ffull[fb], (c >> 1) & 1, abort_flag, err, 128);
+        ok = ok && warp_wait(&S->done[s], (i / STAGES) & 1, abort_flag, err, 128);
+        if (!ok) break;
         fp8_fence_after();
 #pragma unroll
         for (int j = 0; j < CHUNKS; ++j) {
           uint32_t v[16];
-          tmem_ld16(lane_base + b * COLS + column(j), v);
+          tmem_ld(lane_base + b * COLS + column(j), v);
           float4 x[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4*>(&S->factor[fb][f][column(j) + 4 * y]);
@@ -276,11 +268,8 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
           }
         }
         fp8_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S->tempty[b]);
-          if (f == FK - 1 || kb == kb1 - 1) mbar_arrive(&S->fempty[fb]);
-        }
+        warp_arrive(&S->tempty[b]);
+        if (f == FK - 1 || kb == kb1 - 1) warp_arrive(&S->fempty[fb]);
         c += f == FK - 1 || kb == kb1 - 1;
       }
       // Every block of this CTA has been multiplied: the ring's memory is free for the sums.
