@@ -39,22 +39,12 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = kFp8Block;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4, TMEM_COLS = 512;
-#ifndef SW_
-#define SW_ 8
-#endif
-constexpr int SUM_WARPS = SW_, THREADS = 128 + 32 * SUM_WARPS;
-constexpr int GROUPS = SUM_WARPS / 4;         // warpgroups that share a tile's columns
-constexpr int GC = BN / GROUPS;               // columns of a summing thread
-constexpr int LC = GROUPS == 2 ? 32 : 16;     // columns of a TMEM load
-constexpr int FK = 8;   // blocks of K per chunk of factors
+constexpr int SUM_WARPS = 8, THREADS = 128 + 32 * SUM_WARPS;
+constexpr int HN = BN / 2;    // columns of a summing thread: half of the tile's
+constexpr int LC = 32;        // columns of a TMEM load
+constexpr int FK = 8;         // blocks of K per chunk of factors
 // registers: (4 * 72 + 8 * 216) * 32 = 384 * 168, the launch's
-#if SW_ == 8
-#define FP8_GEMM_CONTROL_REGS 72
-#define FP8_GEMM_SUM_REGS 216
-#else
-#define FP8_GEMM_CONTROL_REGS 56
-#define FP8_GEMM_SUM_REGS 104
-#endif
+constexpr int CONTROL_REGS = 72, SUM_REGS = 216;
 
 struct Smem {
   uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves;
@@ -63,7 +53,7 @@ struct Smem {
   int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
   int row_start[kMaxList];
   int rows[kMaxList];
-  float amax[2][GROUPS][BM];    // gate/up: a row's largest |h| per warpgroup, double-buffered by tile
+  float amax[2][2][BM];         // gate/up: a row's largest |h| per half, double-buffered by tile
   float factor[2][FK][2][BM];   // sa * sw of a row: by half of the columns, or for gate and up
 };
 
@@ -159,121 +149,119 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
   };
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8_GEMM_CONTROL_REGS));
-  if (warp == 0) {   // ------------------------------------------------ TMA producer
-    int it = 0;
-    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
-      int g, m, n;
-      decode(t, g, m, n);
-      const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
-      bool stop = false;
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!warp_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121)) {
-          stop = true;
-          break;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
+    if (warp == 0) {   // ------------------------------------------------ TMA producer
+      int it = 0;
+      for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+        int g, m, n;
+        decode(t, g, m, n);
+        const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
+        bool stop = false;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!warp_wait(&S->done[s], ((it / STAGES) & 1) ^ 1, abort_flag, err, 121)) {
+            stop = true;
+            break;
+          }
+          if (elect_one()) {
+            unsigned char* sa = base + s * STAGE_BYTES;
+            unsigned char* sb = sa + A_BYTES;
+            mbar_expect_tx(&S->full[s], STAGE_BYTES);
+            fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
+            fp8_tma_3d(sb, &maps.b[0], &S->full[s], kb * BK, n * TN, z);
+            fp8_tma_3d(sb + B_BYTES / 2, &maps.b[1], &S->full[s], kb * BK, MODE == 0 ? n * TN : n * TN + BN / 2, z);
+          }
+          __syncwarp();
         }
+        if (stop) break;
+      }
+      // drain: wait (bounded) until every issued stage has landed
+      if (lane == 0)
+        for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
+    } else if (warp == 1) {   // ------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = fp8_idesc(BM, BN);
+      const uint64_t desc0 = fp8_desc(smem_u32(base));   // stage s, K step kk: + (s * STAGE_BYTES + kk * 32) / 16
+      // a block starts its sums afresh: the issuer sees blocks, not tiles
+      const long long mine = total_tiles > blockIdx.x ? (total_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+      int it = 0;
+      for (long long left = mine * KB; left > 0; --left, ++it) {
+        const int s = it % STAGES, b = it & 1;
+        if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122)) break;
+        fp8_fence_after();
         if (elect_one()) {
-          unsigned char* sa = base + s * STAGE_BYTES;
-          unsigned char* sb = sa + A_BYTES;
-          mbar_expect_tx(&S->full[s], STAGE_BYTES);
-          fp8_tma_2d(sa, &maps.a, &S->full[s], kb * BK, row0);
-          fp8_tma_3d(sb, &maps.b[0], &S->full[s], kb * BK, n * TN, z);
-          fp8_tma_3d(sb + B_BYTES / 2, &maps.b[1], &S->full[s], kb * BK, MODE == 0 ? n * TN : n * TN + BN / 2, z);
+          const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk) fp8_mma(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+          fp8_commit(&S->done[s]);   // frees the stage and hands the buffer to the sums
         }
         __syncwarp();
       }
-      if (stop) break;
-    }
-    // drain: wait (bounded) until every issued stage has landed
-    if (lane == 0)
-      for (int j = it - STAGES < 0 ? 0 : it - STAGES; j < it; ++j) mbar_drain(&S->full[j % STAGES], (j / STAGES) & 1);
-  } else if (warp == 1) {   // ------------------------------------------- MMA issuer
-    constexpr uint32_t idesc = fp8_idesc(BM, BN);
-    const uint64_t desc0 = fp8_desc(smem_u32(base));   // stage s, K step kk: + (s * STAGE_BYTES + kk * 32) / 16
-    // a block starts its sums afresh: the issuer sees blocks, not tiles
-    const long long mine = total_tiles > blockIdx.x ? (total_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    int it = 0;
-    for (long long left = mine * KB; left > 0; --left, ++it) {
-      const int s = it % STAGES, b = it & 1;
-      if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122)) break;
-      fp8_fence_after();
-      if (elect_one()) {
-        const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
+    } else {   // ---------------------------------------------------------- factors
+      const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
+      const int NB = (p.N + kFp8Block - 1) / kFp8Block;
+      int ch = 0;
+      for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+        int g, m, n;
+        decode(t, g, m, n);
+        const int first = S->row_start[g], last = first + S->rows[g] - 1;
+        const float* sa[2];
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) fp8_mma(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
-        fp8_commit(&S->done[s]);   // frees the stage and hands the buffer to the sums
-      }
-      __syncwarp();
-    }
-  } else {   // ---------------------------------------------------------- factors
-    const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
-    const int NB = (p.N + kFp8Block - 1) / kFp8Block;
-    int ch = 0;
-    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
-      int g, m, n;
-      decode(t, g, m, n);
-      const int first = S->row_start[g], last = first + S->rows[g] - 1;
-      const float* sa[2];
+        for (int i = 0; i < 2; ++i) {   // rows past the group repeat its last
+          int row = min(first + m * BM + r0 + 64 * i, last);
+          if (MODE == 0) row = groups.expert[g] < 0 ? row - p.T * p.k : p.perm[row] / p.k;
+          sa[i] = p.a_scales + (long long)row * KB;
+        }
+        // weight scales: gate and up of the tile's block of I, or the blocks of the tile's two halves
+        const long long wz = groups.z[g] * p.blob;
+        const float* sw[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {   // rows past the group repeat its last
-        int row = min(first + m * BM + r0 + 64 * i, last);
-        if (MODE == 0) row = groups.expert[g] < 0 ? row - p.T * p.k : p.perm[row] / p.k;
-        sa[i] = p.a_scales + (long long)row * KB;
-      }
-      // weight scales: gate and up of the tile's block of I, or the blocks of the tile's two halves
-      const long long wz = groups.z[g] * p.blob;
-      const float* sw[2];
+        for (int i = 0; i < 2; ++i)
+          sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)(MODE == 0 ? n : min(2 * n + i, NB - 1)) * KB;
+        bool ok = true;
+        for (int k0 = 0; k0 < KB; k0 += FK, ++ch) {
+          const int b = ch & 1, kn = min(FK, KB - k0);
+          float w[2][FK], a[2][FK];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)(MODE == 0 ? n : min(2 * n + i, NB - 1)) * KB;
-      bool ok = true;
-      for (int k0 = 0; k0 < KB; k0 += FK, ++ch) {
-        const int b = ch & 1, kn = min(FK, KB - k0);
-        float w[2][FK], a[2][FK];
+          for (int j = 0; j < FK; ++j)
 #pragma unroll
-        for (int j = 0; j < FK; ++j)
+            for (int i = 0; i < 2; ++i) {
+              w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
+              a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
+            }
+          ok = warp_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
+          if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
-            a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
-          }
-        ok = warp_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
+          for (int j = 0; j < FK; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              S->factor[b][j][0][r0 + 64 * i] = a[i][j] * w[0][j];
+              S->factor[b][j][1][r0 + 64 * i] = a[i][j] * w[1][j];
+            }
+          warp_arrive(&S->ffull[b]);
+        }
         if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < FK; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            S->factor[b][j][0][r0 + 64 * i] = a[i][j] * w[0][j];
-            S->factor[b][j][1][r0 + 64 * i] = a[i][j] * w[1][j];
-          }
-        warp_arrive(&S->ffull[b]);
       }
-      if (!ok) break;
     }
-  }
   } else {   // -------------------------------------------------------- sums and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8_GEMM_SUM_REGS));
-    const int q = warp & 3, grp = (warp - 4) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SUM_REGS));
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const int r = q * 32 + lane;               // tile row of this thread
-    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const int NB = (p.N + kFp8Block - 1) / kFp8Block;
-    // warpgroup g sums columns GC g .. of a product tile; columns GC/2 g .. of gate and of up
-    constexpr int NL = GC / LC;   // TMEM loads per block
-    const uint32_t col0 = lane_base + grp * (MODE == 0 ? GC / 2 : GC);
+    constexpr int NL = HN / LC;                // TMEM loads per block
+    // half h sums columns 128 h .. of a product tile; columns 64 h .. of gate and of up
+    const uint32_t col0 = tmem + ((uint32_t)(q * 32) << 16) + half * (MODE == 0 ? HN / 2 : HN);
     auto column = [&](int c) {
       return MODE == 0 ? (c / (NL / 2)) * (BN / 2) + (c % (NL / 2)) * LC : c * LC;
     };
-    const int half = grp * 2 / GROUPS;   // the factor of a product tile's column
     int it = 0, tl = 0, ch = 0;
     for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
       int g, m, n;
       decode(t, g, m, n);
       const bool valid = r < S->rows[g] - m * BM;
       const long long row = S->row_start[g] + (long long)m * BM + r;
-      float acc[GC];
+      float acc[HN];
 #pragma unroll
-      for (int i = 0; i < GC; ++i) acc[i] = 0.f;
+      for (int i = 0; i < HN; ++i) acc[i] = 0.f;
       // The next block's first columns are asked for before this one's last are added, so that
       // the wait for the tensor cores and the load's latency pass behind multiply-adds.
       uint32_t v[2][LC];
@@ -317,22 +305,21 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       }
       if (!ok) break;
       if (MODE == 0) {
-        constexpr int HC = GC / 2;
+        constexpr int HC = HN / 2;   // h columns of this half
         float h[HC], mx = 0.f;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
           h[i] = silu(acc[i]) * acc[HC + i];
           mx = amax_nan(mx, h[i]);
         }
-        S->amax[tl & 1][grp][r] = mx;
+        S->amax[tl & 1][half][r] = mx;
         warp_arrive(&S->halves);
         ok = warp_wait(&S->halves, tl & 1, abort_flag, err, 124);
         if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) mx = amax_nan(mx, S->amax[tl & 1][i][r]);
+        mx = amax_nan(mx, S->amax[tl & 1][half ^ 1][r]);
         const float sc = fp8_scale(mx), inv = 1.0f / sc;
         if (valid) {
-          const int c0 = n * TN + grp * HC;
+          const int c0 = n * TN + half * HC;
           uint8_t* dst = static_cast<uint8_t*>(p.out) + row * p.N + c0;
 #pragma unroll
           for (int j = 0; j < HC / 16; ++j)
@@ -345,18 +332,18 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               }
               *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          if (grp == 0) p.out_scales[row * NB + n] = sc;
+          if (half == 0) p.out_scales[row * NB + n] = sc;
         }
       } else {
-        const int c0 = n * TN + grp * GC;
+        const int c0 = n * TN + half * HN;
         const int es = p.out_bf16 ? 2 : 4;
         unsigned char* dst = static_cast<unsigned char*>(p.out) + (row * p.ldo + c0) * es;
-        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + GC <= p.N) {
+        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + HN <= p.N) {
           // a thread stores its own row, a whole 32-byte sector at a time
           if (valid) {
             if (p.out_bf16) {
 #pragma unroll
-              for (int j = 0; j < GC / 16; ++j) {
+              for (int j = 0; j < HN / 16; ++j) {
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = bf16x2(acc[16 * j + 2 * i], acc[16 * j + 2 * i + 1]);
@@ -364,7 +351,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
               }
             } else {
 #pragma unroll
-              for (int j = 0; j < GC / 8; ++j) {
+              for (int j = 0; j < HN / 8; ++j) {
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[8 * j + i]);
@@ -377,7 +364,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
           // consecutive columns of a row
           const int rows_left = S->rows[g] - m * BM - q * 32;
 #pragma unroll
-          for (int j = 0; j < GC / 32; ++j) {
+          for (int j = 0; j < HN / 32; ++j) {
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);
