@@ -59,7 +59,7 @@ struct Fp8Gemm {
 cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int num_sms,
                             cudaStream_t s);
 // The same product with the weights as the tensor cores' M, for few rows (fp8_stream.cu): nt
-// tokens (16, 32, 64; mode 1: 128) per CTA, K split over clusters of `split` CTAs (1 .. 8, at most
+// tokens (16, 32; mode 0: 64, mode 1: 128) per CTA, K split over clusters of `split` CTAs (1 .. 8, at most
 // the blocks of K), `chunks` CTAs sharing a group's token chunks.  maps.a: mode 0 boxes of one
 // row of x, mode 1 of nt rows.  after_gate_up: this launch directly follows the gate/up launch
 // (mode 0 of this kernel) that writes its rows, and loads weights while that one finishes.

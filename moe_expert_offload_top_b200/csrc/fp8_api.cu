@@ -1,4 +1,6 @@
 // C entry points of the fp8 operators (include/ftmoe.h): argument checks, tensor maps, launches.
+#include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "fp8.hpp"
@@ -48,17 +50,43 @@ int num_sms() {
 struct Plan {
   int nt, split, chunks;
 };
-Plan plan(int mode, long long rows, int groups, int N, int K, int sms) {
-  Plan pl{0, 1, 1};
-  if (rows > (mode == 0 ? 64 : 256)) return pl;
-  const int most = mode == 0 ? 64 : 128;
-  pl.nt = 16;
-  while (pl.nt < rows && pl.nt < most) pl.nt *= 2;
-  pl.chunks = (int)((rows + pl.nt - 1) / pl.nt);
-  const long long tiles = (long long)ftk::fp8_blocks(N) * groups * pl.chunks;
-  const int kb = ftk::fp8_blocks(K);
-  while (pl.split < 8 && 3 * tiles * pl.split < 2 * sms && kb >= 4 * pl.split) pl.split *= 2;
-  return pl;
+// The plan of the least estimated time, in us as measured on a B200.  A CTA of the streaming kernel
+// takes a time of its own (more where K is split: the exchange of the sums) and a time per block of
+// K, less of it where two share an SM (`pair`); an SM runs its CTAs in turn.  The tiles take a
+// fixed time, and per wave a time per block and one for the stores.  No plan is faster than the
+// weights' bytes.  What it decides, measured: 4096 x 4096 weights, 1 row 7.8 against 18.7 on the
+// tiles, 200 rows 16.8 against 21.8, 384 rows 22.9 against 22.1; 100 x 512 x 512 with 16 tokens per
+// CTA and K in four 4.2, with 128 tokens 7.9.
+Plan plan(int mode, long long rows, int groups, int N, int K, int sms, bool aligned_rows) {
+  struct Kind {
+    int nt;
+    double own, own_split, alone, pair;
+  };
+  static const Kind product[3] = {{16, 1.0, 2.0, 0.25, 0.175}, {32, 1.2, 2.0, 0.33, 0.25}, {128, 3.4, 5.2, 0.54, 0.54}};
+  static const Kind gate_up[3] = {{16, 1.0, 2.0, 0.40, 0.30}, {32, 1.2, 2.0, 0.53, 0.40}, {64, 3.4, 5.2, 0.80, 0.80}};
+  const int kb = ftk::fp8_blocks(K), tn = mode == 0 ? 128 : 256;
+  const long long tiles = (rows + 127) / 128 * ((N + tn - 1) / tn) * groups;
+  const double bytes = 2.2 + (mode == 0 ? 2.0 : 1.0) * N * K * groups / 6.0e6;
+  // the tiles of gate/up: after a launch that copies the rows, and no early start for the down product
+  const double fixed = mode == 0 ? 10.0 : 5.0;
+  Plan best{0, 1, 1};
+  double least = fixed + (double)((tiles + sms - 1) / sms) * (0.45 * kb + (aligned_rows ? 1.5 : 8.0));
+  if (least < bytes + fixed - 2.2) least = bytes + fixed - 2.2;
+  for (const Kind& k : mode == 0 ? gate_up : product) {
+    const long long chunks = (rows + k.nt - 1) / k.nt;
+    if (chunks > 64) continue;
+    for (int split = 1; split <= 8 && split <= kb; split *= 2) {
+      const long long ctas = ftk::fp8_blocks(N) * groups * chunks * split, turns = (ctas + sms - 1) / sms;
+      const double per_block = turns == 1 ? k.alone : k.pair;
+      double t = 2.2 + turns * ((split == 1 ? k.own : k.own_split) + per_block * ((kb + split - 1) / split));
+      if (t < bytes) t = bytes;
+      if (t < least) {
+        least = t;
+        best = Plan{k.nt, split, (int)chunks};
+      }
+    }
+  }
+  return best;
 }
 
 int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stream) {
@@ -114,7 +142,7 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
   const int rc = check_device(call, out);
   if (rc != FT_OK) return rc;
   const int sms = num_sms();
-  const Plan pl = plan(1, M, 1, N, K, sms);
+  const Plan pl = plan(1, M, 1, N, K, sms, ldo * (out_is_bf16 ? 2 : 4) % 16 == 0 && aligned(out, 16));
   ftk::Fp8Maps m;
   if (!ftk::encode_map_fp8(&m.a, a, K, M, lda, 0, 0, pl.nt ? pl.nt : 128) ||
       !ftk::encode_map_fp8(&m.b[0], w, K, N, ldw, 1, (uint64_t)ldw * N, 128)) {
@@ -170,41 +198,70 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   }
   const int rc = check_device(call, y);
   if (rc != FT_OK) return rc;
-  const uint64_t rows = (uint64_t)T * top_k + T, n = (uint64_t)H * I, blob = ft_fp8_blob_bytes(H, I);
+  const uint64_t pairs = (uint64_t)T * top_k + T, n = (uint64_t)H * I, blob = ft_fp8_blob_bytes(H, I);
   const size_t sb = 4 * (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
-  // pairs per listed expert, were they spread evenly
   const int sms = num_sms();
-  const long long each = ((long long)T * top_k + n_list - 1) / n_list;
-  const Plan pu = plan(0, each, n_list, I, H, sms), pd = plan(1, each > 64 ? 257 : each, n_list, H, I, sms);
-  ftk::Fp8Maps up, down;
-  if (!(pu.nt ? ftk::encode_map_fp8(&up.a, x, H, T, ldx, 0, 0, 1)
-              : ftk::encode_map_fp8(&up.a, y, H, rows, 4ull * H, 0, 0, 128)) ||
-      !ftk::encode_map_fp8(&up.b[0], w, H, I, H, n_slots, blob, 128) ||
-      !ftk::encode_map_fp8(&up.b[1], w + n, H, I, H, n_slots, blob, 128) ||
-      !ftk::encode_map_fp8(&down.a, h, I, rows, I, 0, 0, pd.nt ? pd.nt : 128) ||
-      !ftk::encode_map_fp8(&down.b[0], w + 2 * n, I, H, I, n_slots, blob, 128)) {
-    ftk::set_step_error(std::string(call) + ": cuTensorMapEncodeTiled failed");
-    return FT_ERR_CUDA;
-  }
-  down.b[1] = down.b[0];
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* ws = w + 3 * n;
   const ftk::Fp8Gemm g{x_scales, {ws, ws + sb}, (long long)blob, offsets, perm, T, top_k, I, H, h, h_scales, I, 0, err};
   const ftk::Fp8Gemm d{h_scales, {ws + 2 * sb, ws + 2 * sb}, (long long)blob, offsets, perm, T, top_k, H, I,
                        y, nullptr, H, 0, err};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The launches of one product of some of the groups, `rows` rows each.  The gate/up tiles find
+  // the pairs' token rows in the rows of y that the down product writes last.
+  const char* what = "launch: ";
+  auto product = [&](int mode, const ftk::GemmGroups& gr, long long rows, bool early) -> cudaError_t {
+    const Plan pl = plan(mode, rows, gr.n, mode == 0 ? I : H, mode == 0 ? H : I, sms, true);
+    const uint32_t box = pl.nt ? pl.nt : 128;
+    ftk::Fp8Maps m;
+    bool ok;
+    if (mode == 0) {
+      ok = (pl.nt ? ftk::encode_map_fp8(&m.a, x, H, T, ldx, 0, 0, 1)
+                  : ftk::encode_map_fp8(&m.a, y, H, pairs, 4ull * H, 0, 0, box)) &&
+           ftk::encode_map_fp8(&m.b[0], w, H, I, H, n_slots, blob, 128) &&
+           ftk::encode_map_fp8(&m.b[1], w + n, H, I, H, n_slots, blob, 128);
+    } else {
+      ok = ftk::encode_map_fp8(&m.a, h, I, pairs, I, 0, 0, box) &&
+           ftk::encode_map_fp8(&m.b[0], w + 2 * n, I, H, I, n_slots, blob, 128);
+      m.b[1] = m.b[0];
+    }
+    if (!ok) {
+      what = "cuTensorMapEncodeTiled: ";
+      return cudaErrorInvalidValue;
+    }
+    if (pl.nt) return ftk::launch_fp8_stream(mode, pl.nt, pl.split, pl.chunks, m, gr, mode == 0 ? g : d, early, s);
+    cudaError_t e = cudaSuccess;
+    if (mode == 0) e = ftk::launch_fp8_gather(x, ldx, gr, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
+    return e == cudaSuccess ? ftk::launch_fp8_gemm(mode, m, gr, mode == 0 ? g : d, sms, s) : e;
+  };
+  // Pairs of a routed expert: the even share and three times its square root, the spread of a
+  // random routing (an expert with more takes its CTAs longer).  The shared expert has T.
+  const int routed = n_list - (seen[0] ? 1 : 0);
+  const double even = routed ? (double)T * top_k / routed : 0.0;
+  const long long each = std::min((long long)T, (long long)std::ceil(even + 3.0 * std::sqrt(even)));
   cudaError_t e;
-  if (pu.nt) {
-    e = ftk::launch_fp8_stream(0, pu.nt, pu.split, pu.chunks, up, groups, g, false, s);
+  if (seen[0] && routed && T > 16 && T > 2 * each && plan(0, each, routed, I, H, sms, true).nt) {
+    // far more rows in the shared expert, and the others stream: its products are launched by
+    // themselves (100 tokens, 64 experts, top 4: 342 -> 279 us); the tiles take any mix at once
+    ftk::GemmGroups some, shared;
+    some.n = 0;
+    shared.n = 1;
+    for (int i = 0; i < n_list; ++i) {
+      ftk::GemmGroups& to = experts[i] < 0 ? shared : some;
+      const int at = experts[i] < 0 ? 0 : some.n++;
+      to.expert[at] = groups.expert[i];
+      to.z[at] = groups.z[i];
+    }
+    e = product(0, some, each, false);
+    if (e == cudaSuccess) e = product(0, shared, T, false);
+    if (e == cudaSuccess) e = product(1, some, each, true);
+    if (e == cudaSuccess) e = product(1, shared, T, false);
   } else {
-    // the pairs' token rows wait in the rows of y that the down product writes last
-    e = ftk::launch_fp8_gather(x, ldx, groups, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
-    if (e == cudaSuccess) e = ftk::launch_fp8_gemm(0, up, groups, g, sms, s);
+    const long long rows = std::max(each, seen[0] ? (long long)T : 0ll);
+    e = product(0, groups, rows, false);
+    if (e == cudaSuccess) e = product(1, groups, rows, true);
   }
-  if (e == cudaSuccess)
-    e = pd.nt ? ftk::launch_fp8_stream(1, pd.nt, pd.split, pd.chunks, down, groups, d, pu.nt > 0, s)
-              : ftk::launch_fp8_gemm(1, down, groups, d, sms, s);
-  return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
+  return e == cudaSuccess ? FT_OK : failed(call, what, e);
 }
 
 }  // extern "C"

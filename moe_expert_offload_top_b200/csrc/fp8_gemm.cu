@@ -57,6 +57,15 @@ struct Smem {
   float factor[2][FK][2][BM];   // sa * sw of a row: by half of the columns, or for gate and up
 };
 
+// Eight words to a 32-byte aligned address, or a 16-byte aligned one.
+FT_DEVICE void st_row(void* p, const uint32_t (&w)[8], bool sector) {
+  if (sector) {
+    st_sector(p, w);
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // v[i] of lane l <-> v[l] of lane i.
 FT_DEVICE void transpose32(uint32_t (&v)[32], int lane) {
 #pragma unroll
@@ -338,8 +347,10 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         const int c0 = n * TN + half * HN;
         const int es = p.out_bf16 ? 2 : 4;
         unsigned char* dst = static_cast<unsigned char*>(p.out) + (row * p.ldo + c0) * es;
-        if (((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0 && c0 + HN <= p.N) {
-          // a thread stores its own row, a whole 32-byte sector at a time
+        if (((p.ldo * es) & 15) == 0 && ((uintptr_t)p.out & 15) == 0) {
+          // a thread stores its own row, a 32-byte sector at a time (two halves where rows are
+          // 16-byte aligned only)
+          const bool sectors = ((p.ldo * es) & 31) == 0 && ((uintptr_t)p.out & 31) == 0;
           if (valid) {
             if (p.out_bf16) {
 #pragma unroll
@@ -347,7 +358,14 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = bf16x2(acc[16 * j + 2 * i], acc[16 * j + 2 * i + 1]);
-                st_sector(dst + 32 * j, w);
+                if (c0 + 16 * j + 16 <= p.N) {
+                  st_row(dst + 32 * j, w, sectors);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    if (c0 + 16 * j + i < p.N)
+                      reinterpret_cast<uint16_t*>(dst)[16 * j + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                }
               }
             } else {
 #pragma unroll
@@ -355,7 +373,13 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
                 uint32_t w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[8 * j + i]);
-                st_sector(dst + 32 * j, w);
+                if (c0 + 8 * j + 8 <= p.N) {
+                  st_row(dst + 32 * j, w, sectors);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (c0 + 8 * j + i < p.N) reinterpret_cast<uint32_t*>(dst)[8 * j + i] = w[i];
+                }
               }
             }
           }

@@ -1,16 +1,16 @@
 // Block-scaled fp8 products for few rows: bound by the weights' bytes.
 //
 // The same functions as fp8_gemm.cu with the operands changed over: 128 weight rows are the
-// M of a tcgen05.mma and up to NT token rows its N (16 .. 128), so that one token costs the
+// M of a tcgen05.mma and up to NT token rows its N (16, 32; gate/up 64, product 128), so that one token costs the
 // tensor cores N = 16 and not a tile of 128 rows.  TMEM lane = weight row, column = token:
 //
 //   acc[n][t] += sw[n / 128][kb] sa[t][kb] * (sum over k in block kb of w[n][k] a[t][k])
 //
-// One CTA per (128 weight rows, expert, NT tokens), two CTAs per SM where registers allow:
+// One CTA per (128 weight rows, expert, NT tokens):
 //   warp 0     TMA producer: the weight tile(s) of a block of K (16 KB; gate and up 32 KB) and
-//              the tokens' 128 bytes each (gate/up: gathered four rows at a time), into a ring
-//              of about 100 KB per CTA.  The ring is what reaches the memory's rate: 200 KB in
-//              flight per SM.
+//              the tokens' 128 bytes each (gate/up: gathered, a lane asking for four rows),
+//              into a ring.  The ring is what reaches the memory's rate: about 200 KB in flight
+//              per SM, in one CTA or two.
 //   warp 1     MMA issuer, into TMEM buffers in turn (256 columns per CTA).
 //   warps 2,3  factors sa * sw of the tokens, four blocks of K at a time, into shared memory.
 //   others     sums: a thread owns a weight row; 16 columns at a time leave TMEM and are added
@@ -18,7 +18,7 @@
 // Few tiles (a narrow product) leave SMs without weights to read, so K is split over the CTAs of
 // a cluster: each leaves its sums in its shared memory, and rank r adds the columns r * NT / S ..
 // of all ranks in rank order (the result does not depend on timing), and stores them.
-// Stores: 128 threads hold 128 consecutive columns of one output row.
+// Stores: a warp holds 128 consecutive columns of one output row, and so a whole scale block of h.
 //
 // Every wait is bounded as in fp8_gemm.cu (codes 126-129); the cluster barriers are reached by
 // every thread whatever its role met.
@@ -34,31 +34,32 @@ constexpr int FK = 4;             // blocks of K per chunk of factors
 constexpr int TMEM_COLS = 256;
 constexpr int MAX_STAGES = 8;
 
-template <int COLS, int NT>
+template <int COLS>
 struct Ctrl {
   uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_STAGES], ffull[2], fempty[2];
   uint32_t tmem_base;
   int abort;
   alignas(16) float factor[2][FK][COLS];
-  float wmax[4][NT];              // gate/up: largest |h| of a token in each of the four warps
 };
 
 template <int MODE, int NT>
 struct Cfg {
   static constexpr int W = MODE == 0 ? 2 : 1;           // weight tiles per block of K
   static constexpr int COLS = W * NT;                   // accumulator columns
-  static constexpr int SW = COLS > 64 ? 2 : 1;          // summing warpgroups
+  static constexpr int SW = COLS > 32 ? 2 : 1;          // summing warpgroups
   static constexpr int THREADS = 128 + 128 * SW;
-  static constexpr int PER_SM = COLS > 64 ? 1 : 2;
+  // Two CTAs hide one's set-up and stores behind the other's loads; the gate/up tiles are twice as
+  // long and do better with the whole ring to one (FFN of one token, 7 experts: 38.2 -> 35.6 us).
+  static constexpr int PER_SM = MODE == 0 || COLS > 32 ? 1 : 2;
   static constexpr int STAGE = W * WTILE + NT * BK;
   // shared memory of an SM (228 KB, 1 KB of it reserved per CTA) over its CTAs
   static constexpr int LIMIT = (228 * 1024) / PER_SM - 1024;
-  static constexpr int FIT = (LIMIT - 1024 - (int)sizeof(Ctrl<COLS, NT>)) / STAGE;
+  static constexpr int FIT = (LIMIT - 1024 - (int)sizeof(Ctrl<COLS>)) / STAGE;
   static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
   // Not more buffers than stages: the sums follow the blocks by the phases of the stages'
   // barriers, and may be behind by the number of buffers.
   static constexpr int BUFS = TMEM_COLS / COLS < STAGES ? TMEM_COLS / COLS : STAGES;
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(Ctrl<COLS, NT>);
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(Ctrl<COLS>);
   static_assert(STAGES * STAGE >= COLS * 128 * 4, "the sums of a tile wait in the ring's memory");
 };
 
@@ -66,13 +67,31 @@ FT_DEVICE void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A float at this CTA's shared address, in the CTA `rank` of the cluster.
-FT_DEVICE float ld_rank(uint32_t addr, int rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+// Four consecutive sums, added over the cluster's CTAs in rank order; all loads in flight at once.
+FT_DEVICE void total(const float* p, int split, float (&v)[4]) {
+  if (split == 1) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    return;
+  }
+  const uint32_t at = smem_u32(p);
+  float f[8][4];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(r));
+      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(f[r][0]), "=f"(f[r][1]), "=f"(f[r][2]), "=f"(f[r][3]) : "r"(a) : "memory");
+    }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = 0.f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] += f[r][x];
+    }
 }
 
 template <int MODE, int NT>
@@ -83,7 +102,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
   constexpr int W = C::W, COLS = C::COLS, STAGES = C::STAGES, BUFS = C::BUFS, STAGE = C::STAGE;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  Ctrl<COLS, NT>* S = reinterpret_cast<Ctrl<COLS, NT>*>(base + STAGES * STAGE);
+  Ctrl<COLS>* S = reinterpret_cast<Ctrl<COLS>*>(base + STAGES * STAGE);
   float* part = reinterpret_cast<float*>(base);   // [COLS][128] sums, once the ring is drained
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (p.K + BK - 1) / BK, NB = (p.N + BK - 1) / BK;
@@ -144,12 +163,12 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
   for (int t0 = blockIdx.z * NT; t0 < rows; t0 += gridDim.z * NT) {
     const int valid = min(NT, rows - t0), row0 = first + t0;
     if (warp == 0) {   // -------------------------------------------------- TMA producer
-      int tok[(NT + 31) / 32];
-      if (MODE == 0) {   // tokens past the last repeat it
+      int tok[4];
+      if (MODE == 0) {   // lane l < NT / 4 gathers tokens 4 l .. 4 l + 3; tokens past the last repeat it
 #pragma unroll
-        for (int i = 0; i < (NT + 31) / 32; ++i) {
-          const int q = row0 + min(i * 32 + lane, valid - 1);
-          tok[i] = e < 0 ? q - p.T * p.k : p.perm[q] / p.k;
+        for (int x = 0; x < 4; ++x) {
+          const int q = row0 + min(4 * lane + x, valid - 1);
+          tok[x] = e < 0 ? q - p.T * p.k : p.perm[q] / p.k;
         }
       }
       int i = it;
@@ -162,18 +181,9 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
           if (MODE == 1) fp8_tma_2d(sw + W * WTILE, &maps.a, &S->full[s], kb * BK, row0);
         }
         __syncwarp();
-        if (MODE == 0) {
-#pragma unroll 1
-          for (int j = 0; j < NT / 4; ++j) {
-            const int v = NT > 32 && j >= 8 ? tok[(NT + 31) / 32 - 1] : tok[0];
-            const int l = (4 * j) & 31;
-            const int a0 = __shfl_sync(0xFFFFFFFFu, v, l), a1 = __shfl_sync(0xFFFFFFFFu, v, l + 1);
-            const int a2 = __shfl_sync(0xFFFFFFFFu, v, l + 2), a3 = __shfl_sync(0xFFFFFFFFu, v, l + 3);
-            if (elect_one())
-              fp8_tma_gather4(sw + W * WTILE + j * 4 * BK, &maps.a, &S->full[s], kb * BK, a0, a1, a2, a3);
-            __syncwarp();
-          }
-        }
+        if (MODE == 0 && lane < NT / 4)
+          fp8_tma_gather4(sw + W * WTILE + lane * 4 * BK, &maps.a, &S->full[s], kb * BK, tok[0], tok[1], tok[2], tok[3]);
+        __syncwarp();
       }
       // drain: wait (bounded) until every issued stage has landed
       if (lane == 0)
@@ -255,16 +265,14 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         for (int j = 0; j < CHUNKS; ++j) {
           uint32_t v[16];
           tmem_ld(lane_base + b * COLS + column(j), v);
-          float4 x[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4*>(&S->factor[fb][f][column(j) + 4 * y]);
           tmem_wait();
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            fma_col(acc[16 * j + 4 * y], v[4 * y], x[y].x);
-            fma_col(acc[16 * j + 4 * y + 1], v[4 * y + 1], x[y].y);
-            fma_col(acc[16 * j + 4 * y + 2], v[4 * y + 2], x[y].z);
-            fma_col(acc[16 * j + 4 * y + 3], v[4 * y + 3], x[y].w);
+            const float4 x = *reinterpret_cast<const float4*>(&S->factor[fb][f][column(j) + 4 * y]);
+            fma_col(acc[16 * j + 4 * y], v[4 * y], x.x);
+            fma_col(acc[16 * j + 4 * y + 1], v[4 * y + 1], x.y);
+            fma_col(acc[16 * j + 4 * y + 2], v[4 * y + 2], x.z);
+            fma_col(acc[16 * j + 4 * y + 3], v[4 * y + 3], x.w);
           }
         }
         fp8_fence_before();
@@ -283,55 +291,53 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
     ch += (kb1 - kb0 + FK - 1) / FK;
     if (split > 1) cluster_sync(); else __syncthreads();
 
-    // columns of this rank, added over the ranks
-    const int r = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
-    const int c0 = NT * rank / split, c1 = min(NT * (rank + 1) / split, valid);
-    const int col = n * 128 + r;
-    auto total = [&](int c) {
-      const uint32_t at = smem_u32(part + c * 128 + r);
-      if (split == 1) return part[c * 128 + r];
-      float v[8], sum = 0.f;
+    // Columns of this rank, added over the ranks: a warp takes a token, a lane four weight rows.
+    if (warp >= 4) {
+      const int c1 = min(NT * (rank + 1) / split, valid);
+      const int col = n * 128 + 4 * lane;
+#pragma unroll (MODE == 1 ? 2 : 1)
+      for (int c = NT * rank / split + warp - 4; c < c1; c += 4 * C::SW) {
+        const long long row = row0 + c;
+        float v[4];
+        total(part + c * 128 + 4 * lane, split, v);
+        if constexpr (MODE == 1) {
+          const long long at = row * p.ldo + col;
+          if (p.out_bf16) {
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+            const uint32_t lo = bf16x2(v[0], v[1]), hi = bf16x2(v[2], v[3]);
+            if (col + 4 <= p.N && ((uintptr_t)dst & 7) == 0) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+            } else {
+              const uint32_t w[2] = {lo, hi};
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x < split) v[x] = ld_rank(at, x);
+              for (int x = 0; x < 4; ++x)
+                if (col + x < p.N) dst[x] = (uint16_t)(w[x >> 1] >> (16 * (x & 1)));
+            }
+          } else {
+            float* dst = static_cast<float*>(p.out) + at;
+            if (col + 4 <= p.N && ((uintptr_t)dst & 15) == 0) {
+              *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x < split) sum += v[x];
-      return sum;
-    };
-    if (MODE == 1) {
-      if (warp >= 4) {
-        for (int c = c0 + half; c < c1; c += C::SW) {
-          const float v = total(c);
-          const long long at = (long long)(row0 + c) * p.ldo + col;
-          if (col < p.N) {
-            if (p.out_bf16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)bf16x2(v, 0.f);
-            else static_cast<float*>(p.out)[at] = v;
+              for (int x = 0; x < 4; ++x)
+                if (col + x < p.N) dst[x] = v[x];
+            }
           }
-        }
-      }
-    } else {
-      if (warp >= 4) {
-        for (int c = c0 + half; c < c1; c += C::SW) {
-          const float h = silu(total(c)) * total(NT + c);
-          float m = amax_nan(0.f, h);
+        } else {
+          float u[4], m = 0.f;
+          total(part + (NT + c) * 128 + 4 * lane, split, u);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x] = silu(v[x]) * u[x];
+            m = amax_nan(m, v[x]);
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = amax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          if (lane == 0) S->wmax[warp & 3][c] = m;
-          part[c * 128 + r] = h;   // only this thread reads this sum of this rank
-        }
-      }
-      __syncthreads();
-      if (warp >= 4) {
-        for (int c = c0 + half; c < c1; c += C::SW) {
-          float m = S->wmax[0][c];
-#pragma unroll
-          for (int x = 1; x < 4; ++x) m = amax_nan(m, S->wmax[x][c]);
-          const float sc = fp8_scale(m);
-          const long long row = row0 + c;
-          if (col < p.N)
-            static_cast<uint8_t*>(p.out)[row * p.N + col] = (uint8_t)e4m3x2(part[c * 128 + r] * (1.0f / sc), 0.f);
-          if (r == 0) p.out_scales[row * NB + n] = sc;
+          const float sc = fp8_scale(m), inv = 1.0f / sc;
+          if (col < p.N)   // N is a multiple of 16
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.N + col) =
+                e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+          if (lane == 0) p.out_scales[row * NB + n] = sc;
         }
       }
     }
@@ -387,7 +393,6 @@ cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8
   switch (nt) {
     case 16: return launch_nt<1, 16>(maps, groups, p, split, chunks, after_gate_up, s);
     case 32: return launch_nt<1, 32>(maps, groups, p, split, chunks, after_gate_up, s);
-    case 64: return launch_nt<1, 64>(maps, groups, p, split, chunks, after_gate_up, s);
     default: return launch_nt<1, 128>(maps, groups, p, split, chunks, after_gate_up, s);
   }
 }
