@@ -67,8 +67,7 @@ cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8
                               const Fp8Gemm& p, bool after_gate_up, cudaStream_t s);
 // dst + q * stride = the H bytes of pair q's token row, for the pairs of the groups.
 cudaError_t launch_fp8_gather(const void* x, long long ldx, const GemmGroups& groups, const int* offsets,
-                              const int* perm, int T, int k, int H, void* dst, long long stride, int num_sms,
-                              cudaStream_t s);
+                              const int* perm, int T, int k, int H, void* dst, long long stride, cudaStream_t s);
 // uint8 tensor map [depth][rows][inner], 128-byte swizzle, boxes of 128 bytes x box_rows x 1.
 bool encode_map_fp8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
                     uint64_t depth, uint64_t depth_bytes, uint32_t box_rows);

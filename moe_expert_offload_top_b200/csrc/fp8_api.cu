@@ -231,7 +231,7 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
     }
     if (pl.nt) return ftk::launch_fp8_stream(mode, pl.nt, pl.split, pl.chunks, m, gr, mode == 0 ? g : d, early, s);
     cudaError_t e = cudaSuccess;
-    if (mode == 0) e = ftk::launch_fp8_gather(x, ldx, gr, offsets, perm, T, top_k, H, y, 4ll * H, sms, s);
+    if (mode == 0) e = ftk::launch_fp8_gather(x, ldx, gr, offsets, perm, T, top_k, H, y, 4ll * H, s);
     return e == cudaSuccess ? ftk::launch_fp8_gemm(mode, m, gr, mode == 0 ? g : d, sms, s) : e;
   };
   // Pairs of a routed expert: the even share and three times its square root, the spread of a

@@ -458,12 +458,12 @@ cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& gro
 }
 
 cudaError_t launch_fp8_gather(const void* x, long long ldx, const GemmGroups& groups, const int* offsets,
-                              const int* perm, int T, int k, int H, void* dst, long long stride, int num_sms,
-                              cudaStream_t s) {
+                              const int* perm, int T, int k, int H, void* dst, long long stride, cudaStream_t s) {
   if (groups.n <= 0 || T <= 0) return cudaSuccess;
-  // enough warps to fill the SMs, split evenly over the groups; none beyond a group's possible rows
-  const int want = (8 * num_sms + groups.n - 1) / groups.n, most = (T + 7) / 8;
-  const dim3 grid(want < most ? want : most, groups.n);
+  // 32 rows per block, and blocks for the rows that a group can have: those past its rows leave at
+  // once (few blocks per group made the shared expert's, with every token, the last to finish)
+  const int blocks = (T + 31) / 32;
+  const dim3 grid(blocks < 1024 ? blocks : 1024, groups.n);
   fp8_gather_kernel<<<grid, 256, 0, s>>>(static_cast<const uint8_t*>(x), ldx, groups, offsets, perm, T, k, H,
                                          static_cast<uint8_t*>(dst), stride);
   return cudaGetLastError();

@@ -13,7 +13,7 @@
 // through shared memory.  Aligned rows: a thread owns 16 consecutive columns per chunk (32-byte
 // loads), a scale block is 8 lanes; with 8 columns per thread the two divisions and the
 // maximum's exchange, the same work per thread, kept the issue slots half busy.  Others: a warp
-// owns four scale blocks per chunk, lane l the columns l, l+32, .. of each, so that element
+// owns two scale blocks per chunk, lane l the columns l, l+32, .. of each, so that element
 // loads and byte stores still coalesce.
 #include "fp8.hpp"
 #include "fp8_common.cuh"
@@ -68,12 +68,13 @@ FT_DEVICE void store16(void* p, long long i, const float* v) {
     }
   }
 }
-constexpr int E = 16;         // elements of a thread per chunk
-constexpr int UNIT = 32 * E;  // columns of a warp per chunk
+// elements of a thread per chunk; a warp's columns per chunk are 32 times as many
+constexpr int elements(bool vec) { return vec ? 16 : 8; }
 
 // blockDim = (tpr, rows per block).  CH: chunks a thread holds.
 template <bool BF16, bool NORM, bool VEC, int CH>
 __global__ void __launch_bounds__(1024) rows_fp8_kernel(const __grid_constant__ RowsFp8 p) {
+  constexpr int E = elements(VEC);
   __shared__ float part[32];
   const int tpr = blockDim.x, t = threadIdx.x;
   const int warp = t >> 5, lane = t & 31, warps = tpr >> 5;
@@ -210,8 +211,10 @@ template <bool BF16, bool NORM, bool VEC>
 cudaError_t launch_rows(const RowsFp8& p, int ch, dim3 grid, dim3 block, cudaStream_t s) {
   if (ch == 1)
     rows_fp8_kernel<BF16, NORM, VEC, 1><<<grid, block, 0, s>>>(p);
-  else
+  else if (VEC || ch == 2)
     rows_fp8_kernel<BF16, NORM, VEC, 2><<<grid, block, 0, s>>>(p);
+  else
+    rows_fp8_kernel<BF16, NORM, VEC, VEC ? 2 : 4><<<grid, block, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <bool BF16, bool NORM>
@@ -225,12 +228,15 @@ cudaError_t launch_rows(const RowsFp8& p, bool vec, int ch, dim3 grid, dim3 bloc
 cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, cudaStream_t s) {
   if (p.T <= 0) return cudaSuccess;
   auto aligned = [](const void* q, int bytes) { return ((uintptr_t)q & (bytes - 1)) == 0; };
-  const bool vec = p.H % E == 0 && p.ldx % E == 0 && aligned(p.x, 32) &&
-                   ((!p.residual && !p.residual_out) || p.ldr % E == 0) && aligned(p.residual, 32) &&
+  const bool vec = p.H % 16 == 0 && p.ldx % 16 == 0 && aligned(p.x, 32) &&
+                   ((!p.residual && !p.residual_out) || p.ldr % 16 == 0) && aligned(p.residual, 32) &&
                    aligned(p.residual_out, 32) && aligned(p.weight, 32) && aligned(p.y, 32) &&
                    (!p.q || (p.ldq % 16 == 0 && aligned(p.q, 16)));
   // one chunk per thread while a block can hold the row's threads: the shortest way from load to store
-  const int units = (p.H + UNIT - 1) / UNIT, ch = units <= 32 ? 1 : 2, warps = (units + ch - 1) / ch;
+  const int unit = 32 * elements(vec), units = (p.H + unit - 1) / unit;
+  int ch = 1;
+  while ((units + ch - 1) / ch > 32) ch *= 2;
+  const int warps = (units + ch - 1) / ch;
   const int rows = warps >= 4 ? 1 : 4 / warps;
   const dim3 block(warps * 32, rows), grid((unsigned)(((long long)p.T + rows - 1) / rows));
   if (p.weight)
