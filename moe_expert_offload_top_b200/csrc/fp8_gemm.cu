@@ -140,28 +140,28 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
   __syncthreads();
   fp8_fence_after();
   const uint32_t tmem = S->tmem_base;
-  const long long total_tiles = (long long)S->mt_start[groups.n] * n_tiles;
+  const int total_tiles = S->mt_start[groups.n] * n_tiles;   // times 2^15 outputs: far below 2^31
   volatile int* abort_flag = &S->abort;
 
   // tile -> (group, m-tile, n-tile): the M-tiles that share a weight tile run back to back
-  auto decode = [&](long long t, int& g, int& m, int& n) {
+  auto decode = [&](int t, int& g, int& m, int& n) {
     int lo = 0, hi = groups.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((long long)S->mt_start[mid] * n_tiles <= t) lo = mid; else hi = mid - 1;
+      if (S->mt_start[mid] * n_tiles <= t) lo = mid; else hi = mid - 1;
     }
     g = lo;
-    const long long local = t - (long long)S->mt_start[g] * n_tiles;
+    const int local = t - S->mt_start[g] * n_tiles;
     const int mtg = S->mt_start[g + 1] - S->mt_start[g];
-    n = (int)(local / mtg);
-    m = (int)(local - (long long)n * mtg);
+    n = local / mtg;
+    m = local - n * mtg;
   };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
     if (warp == 0) {   // ------------------------------------------------ TMA producer
       int it = 0;
-      for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+      for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
         int g, m, n;
         decode(t, g, m, n);
         const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
@@ -191,9 +191,9 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       constexpr uint32_t idesc = fp8_idesc(BM, BN);
       const uint64_t desc0 = fp8_desc(smem_u32(base));   // stage s, K step kk: + (s * STAGE_BYTES + kk * 32) / 16
       // a block starts its sums afresh: the issuer sees blocks, not tiles
-      const long long mine = total_tiles > blockIdx.x ? (total_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+      const int mine = total_tiles > (int)blockIdx.x ? (total_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
       int it = 0;
-      for (long long left = mine * KB; left > 0; --left, ++it) {
+      for (long long left = (long long)mine * KB; left > 0; --left, ++it) {
         const int s = it % STAGES, b = it & 1;
         if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122)) break;
         fp8_fence_after();
@@ -209,7 +209,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
       const int NB = (p.N + kFp8Block - 1) / kFp8Block;
       int ch = 0;
-      for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+      for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
         int g, m, n;
         decode(t, g, m, n);
         const int first = S->row_start[g], last = first + S->rows[g] - 1;
@@ -263,11 +263,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       return MODE == 0 ? (c / (NL / 2)) * (BN / 2) + (c % (NL / 2)) * LC : c * LC;
     };
     int it = 0, tl = 0, ch = 0;
-    for (long long t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
-      int g, m, n;
-      decode(t, g, m, n);
-      const bool valid = r < S->rows[g] - m * BM;
-      const long long row = S->row_start[g] + (long long)m * BM + r;
+    for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x, ++tl) {
       float acc[HN];
 #pragma unroll
       for (int i = 0; i < HN; ++i) acc[i] = 0.f;
@@ -313,6 +309,10 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         if (!ok) break;
       }
       if (!ok) break;
+      int g, m, n;   // not before: the loop has no register to spare for them
+      decode(t, g, m, n);
+      const bool valid = r < S->rows[g] - m * BM;
+      const long long row = S->row_start[g] + (long long)m * BM + r;
       if (MODE == 0) {
         constexpr int HC = HN / 2;   // h columns of this half
         float h[HC], mx = 0.f;
