@@ -23,7 +23,17 @@
 //               lines per warp cost half of their time.)
 //   warps 4-11  sums: warp w reads TMEM lanes 32 (w % 4).. of one half of the columns, adds
 //               them to 128 sums per thread, and at the end of a tile stores them.  These warps
-//               take 216 registers each from the 168 of the launch, the other four keep 72.
+//               take 224 registers each from the 168 of the launch, the other four keep 56.  The
+//               loop must not spill: the reloads miss the small L1 beside the ring (8 bytes of
+//               spill cost 10 % of the kernel).
+//
+// What bounds it: 8192 x 7168 x 4096 takes 240 us, 2.0 PFLOP/s (cuBLAS reaches 3.3 at 8192^3 with one
+// scale per tensor, that is, without leaving TMEM).  The tensor cores alone would take 515 cycles
+// per block of K (616 with the loads running); the loop takes about 850, because a TMEM buffer is
+// free only after release -> issue (200) -> its MMAs and commit (700 to 800) -> loads and
+// three quarters of the multiply-adds (600), and two buffers of 256 columns fill TMEM.  Tried and
+// slower: halves of N = 128 with two buffers each (the shared-memory reads of A double), 16
+// summing warps (spills), two CTAs per SM with 128 x 128 tiles, paired multiply-adds (moves).
 // gate/up tiles hold 128 gate and 128 up columns; each half of the warps takes 64 columns of
 // both, so silu(gate) * up stays inside a thread.
 //
@@ -43,8 +53,8 @@ constexpr int SUM_WARPS = 8, THREADS = 128 + 32 * SUM_WARPS;
 constexpr int HN = BN / 2;    // columns of a summing thread: half of the tile's
 constexpr int LC = 32;        // columns of a TMEM load
 constexpr int FK = 8;         // blocks of K per chunk of factors
-// registers: (4 * 72 + 8 * 216) * 32 = 384 * 168, the launch's
-constexpr int CONTROL_REGS = 72, SUM_REGS = 216;
+// registers: (4 * 56 + 8 * 224) * 32 = 384 * 168, the launch's
+constexpr int CONTROL_REGS = 56, SUM_REGS = 224;
 
 struct Smem {
   uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves;
@@ -228,24 +238,29 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
           sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)(MODE == 0 ? n : min(2 * n + i, NB - 1)) * KB;
         bool ok = true;
         for (int k0 = 0; k0 < KB; k0 += FK, ++ch) {
-          const int b = ch & 1, kn = min(FK, KB - k0);
-          float w[2][FK], a[2][FK];
-#pragma unroll
-          for (int j = 0; j < FK; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              w[i][j] = j < kn ? sw[i][k0 + j] : 0.f;
-              a[i][j] = j < kn ? sa[i][k0 + j] : 0.f;
-            }
+          const int b = ch & 1;
           ok = warp_wait(&S->fempty[b], ((ch >> 1) & 1) ^ 1, abort_flag, err, 125);
           if (!ok) break;
+#pragma unroll 1
+          for (int j0 = 0; j0 < FK; j0 += 4) {   // four blocks at a time: these warps have few registers
+            float w[2][4], a[2][4];
 #pragma unroll
-          for (int j = 0; j < FK; ++j)
+            for (int j = 0; j < 4; ++j) {
+              const int kb = min(k0 + j0 + j, KB - 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              S->factor[b][j][0][r0 + 64 * i] = a[i][j] * w[0][j];
-              S->factor[b][j][1][r0 + 64 * i] = a[i][j] * w[1][j];
+              for (int i = 0; i < 2; ++i) {
+                w[i][j] = sw[i][kb];
+                a[i][j] = sa[i][kb];
+              }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                S->factor[b][j0 + j][0][r0 + 64 * i] = a[i][j] * w[0][j];
+                S->factor[b][j0 + j][1][r0 + 64 * i] = a[i][j] * w[1][j];
+              }
+          }
           warp_arrive(&S->ffull[b]);
         }
         if (!ok) break;
@@ -293,7 +308,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
             tmem_ld(ta + column(c + 1), v[(c + 1) & 1]);
           } else {
             fp8_fence_before();
-            warp_arrive(&S->tempty[b]);   // every lane's values are in registers
+            if (lane == 0) mbar_arrive(&S->tempty[b]);   // the loads were the whole warp's: all have landed
             const bool chunk_done = j == FK - 1 || kb == KB - 1;
             if (chunk_done) warp_arrive(&S->fempty[fb]);
             ch += chunk_done;
