@@ -333,7 +333,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         float h[HC], mx = 0.f;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          h[i] = silu(acc[i]) * acc[HC + i];
+          h[i] = silu_fast(acc[i]) * acc[HC + i];
           mx = amax_nan(mx, h[i]);
         }
         S->amax[tl & 1][half][r] = mx;

@@ -328,7 +328,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
           total(part + (NT + c) * 128 + 4 * lane, split, u);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            v[x] = silu(v[x]) * u[x];
+            v[x] = silu_fast(v[x]) * u[x];
             m = amax_nan(m, v[x]);
           }
 #pragma unroll
