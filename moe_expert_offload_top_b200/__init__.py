@@ -374,8 +374,8 @@ def ft_expert_ffn_fp8(x, ldx, x_scales, T, H, I, top_k, weights, n_slots, expert
     if len(experts) != len(slots):
         raise ValueError("experts and slots must have the same length")
     n = len(experts)
-    ex = _int_array(experts or [0])
-    sl = _int_array(slots or [0])
+    ex = _int_array(list(experts) or [0])
+    sl = _int_array(list(slots) or [0])
     return _check(None, _lib.ft_expert_ffn_fp8(
         _p(x), ldx, _p(x_scales), T, H, I, top_k, _p(weights), n_slots, ctypes.cast(ex, ctypes.c_void_p),
         ctypes.cast(sl, ctypes.c_void_p), n, _p(offsets), _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _s(stream)))

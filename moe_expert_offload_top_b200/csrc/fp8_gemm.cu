@@ -444,7 +444,16 @@ __global__ void __launch_bounds__(256) fp8_gather_kernel(const uint8_t* x, long 
     const int tok = e >= 0 ? perm[q] / k : q - T * k;
     const uint4* from = reinterpret_cast<const uint4*>(x + tok * ldx);
     uint4* to = reinterpret_cast<uint4*>(dst + q * stride);
-    for (int i = lane; i < H / 16; i += 32) to[i] = from[i];
+    const int n = H / 16;
+    for (int i = lane; i < n; i += 128) {   // four loads in flight per lane
+      uint4 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (i + 32 * x < n) v[x] = from[i + 32 * x];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (i + 32 * x < n) to[i + 32 * x] = v[x];
+    }
   }
 }
 

@@ -341,6 +341,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         }
       }
     }
+    __syncwarp();
     // the sums have been read, by the other ranks too; the ring is the TMA's again
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (split > 1) cluster_sync(); else __syncthreads();

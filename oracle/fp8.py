@@ -98,7 +98,8 @@ def product_bound(l1, K):
 
 
 def silu(a):
-    return a / (1.0 + np.exp(-a))
+    with np.errstate(over="ignore"):   # exp(-a) = inf: the quotient is 0
+        return a / (1.0 + np.exp(-a))
 
 
 def quantize_weight(w):

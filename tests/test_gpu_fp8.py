@@ -358,7 +358,9 @@ FFN_SHAPES = [  # T, H, I, E, k, shared, empty, skew
     (1, 256, 128, 4, 2, False, (), 0.0), (1, 128, 128, 1, 1, True, (), 0.0), (1, 16, 16, 3, 3, True, (), 0.0),
     (5, 144, 80, 6, 2, True, (0, 3), 0.0), (16, 512, 384, 8, 4, False, (), 1.0), (17, 256, 128, 2, 1, True, (), 0.0),
     (33, 400, 144, 5, 2, False, (4,), 2.0), (64, 256, 256, 4, 2, True, (), 0.0), (130, 384, 272, 3, 2, True, (1,), 0.0),
-    (300, 256, 128, 16, 4, True, (2, 15), 2.0), (700, 512, 256, 4, 2, False, (), 0.5), (129, 128, 640, 2, 2, True, (), 0.0)]
+    (300, 256, 128, 16, 4, True, (2, 15), 2.0), (700, 512, 256, 4, 2, False, (), 0.5), (129, 128, 640, 2, 2, True, (), 0.0),
+    # the shared expert launched apart from experts with few tokens
+    (40, 256, 256, 16, 2, True, (), 0.0), (100, 512, 272, 32, 2, True, (3,), 1.0)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k,shared,empty,skew", FFN_SHAPES)
@@ -386,6 +388,14 @@ def test_expert_ffn_many_tiles_per_cta():
 
 def test_expert_ffn_one_expert_owns_every_pair():
     f = Ffn(150, 256, 128, 3, 1, False, seed=11, empty=(0, 2))
+    f.run()
+    f.check()
+
+
+@pytest.mark.parametrize("T,H,I", [(60, 256, 128), (47, 1024, 144)])
+def test_expert_ffn_crowded_expert_in_a_long_list(T, H, I):
+    """One of 32 experts has every token, where the even share is two: its CTAs take its tokens in turn."""
+    f = Ffn(T, H, I, 32, 1, False, seed=13, empty=tuple(e for e in range(32) if e != 7))
     f.run()
     f.check()
 
@@ -459,6 +469,78 @@ def test_layer_on_fp8_rows():
     check_codes(_bytes(mq), _np(ms), _np(mixed), 0.0)
     ref, l1 = fp8.product(fp8.decode(_bytes(mq)), _np(ms), fp8.decode(wq), ws)
     assert (np.abs(_np(out) - ref) <= fp8.product_bound(l1, H)).all()
+
+
+def test_rows_and_products_past_2_to_31_elements():
+    """Row offsets need 64 bits; the last rows are checked."""
+    T, H = 70000, 32752
+    x = torch.randn((1, H), device=DEV).bfloat16().repeat(T, 1)
+    x[T - 2] *= 3
+    q, s = torch.zeros((T, H), dtype=torch.uint8, device=DEV), torch.zeros((T, fp8.blocks(H)), device=DEV)
+    ft.ft_quantize_fp8(x, H, True, T, H, q, H, s)
+    check_codes(_bytes(q[T - 3:]), _np(s[T - 3:]), _np(x[T - 3:]), 0.0)
+    del x, q, s
+    gen = torch.Generator().manual_seed(8)
+    M, N, K = 66000, 33000, 16
+    a, w = _operand(1, K, K, gen).repeat(M, 1), _operand(N, K, K, gen)
+    a[M - 2] = _operand(1, K, K, gen)
+    sa, sw = _scales((M, 1), gen), _scales((fp8.blocks(N), 1), gen)
+    out, err = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV), _err()
+    ft.ft_gemm_fp8(a, K, sa, w, K, sw, M, N, K, True, out, N, err)
+    ref, l1 = fp8.product(fp8.decode(_bytes(a[M - 3:])), _np(sa[M - 3:]), fp8.decode(_bytes(w)), _np(sw))
+    tol = fp8.product_bound(l1, K) + UBF * np.abs(ref) * (1 + UBF)
+    assert err.item() == 0 and (np.abs(_np(out[M - 3:]) - ref) <= tol).all()
+
+
+def test_ffn_past_2_to_31_elements():
+    T, H, I, E = 40000, 7168, 128, 8      # every token takes every expert: 320000 rows of y and 40000 shared
+    gen = torch.Generator().manual_seed(4)
+    rng = np.random.default_rng(4)
+    row = _operand(1, H, H, gen)
+    x = row.repeat(T, 1)
+    x[T - 1] = _operand(1, H, H, gen)
+    xs = _scales((T, H // 128), gen)
+    raw = [fp8.blob(*[rng.standard_normal(s) * 0.05 for s in ((I, H), (I, H), (H, I))]) for _ in range(E + 1)]
+    weights = torch.from_numpy(np.stack(raw)).to(DEV)
+    offsets = (torch.arange(E + 1, device=DEV) * T).int()
+    perm = (torch.arange(T, device=DEV)[None, :] * E + torch.arange(E, device=DEV)[:, None]).reshape(-1).int()
+    rows = T * E + T
+    h, hs = torch.zeros((rows, I), dtype=torch.uint8, device=DEV), torch.zeros((rows, 1), device=DEV)
+    y, err = torch.zeros((rows, H), device=DEV), _err()
+    ft.ft_expert_ffn_fp8(x, H, xs, T, H, I, E, weights, E + 1, list(range(E)) + [-1], list(range(E + 1)), offsets, perm,
+                         h, hs, y, err)
+    assert err.item() == 0
+    for e in (0, E - 1, E):          # E: the shared expert
+        for t in (0, T - 2, T - 1):
+            at = e * T + t
+            (g, sg), (u, su), (d, sd) = fp8.blob_parts(raw[e], H, I)
+            xv, sv = fp8.decode(_bytes(x[t:t + 1])), _np(xs[t:t + 1])
+            a, la = fp8.product(xv, sv, g, sg)
+            b, lb = fp8.product(xv, sv, u, su)
+            ref = fp8.silu(a) * b
+            bound = (1.1 * fp8.product_bound(la, H) * (np.abs(b) + fp8.product_bound(lb, H)) +
+                     np.abs(fp8.silu(a)) * fp8.product_bound(lb, H) + 8 * U32 * np.abs(ref))
+            check_codes(_bytes(h[at:at + 1]), _np(hs[at:at + 1]), ref, 0.0, bound.max(1, keepdims=True))
+            yr, ly = fp8.product(fp8.decode(_bytes(h[at:at + 1])), _np(hs[at:at + 1]), d, sd)
+            assert (np.abs(_np(y[at:at + 1]) - yr) <= fp8.product_bound(ly, I)).all()
+
+
+def test_ffn_streams_at_once():
+    """Calls on several streams, each with its own rows, give the bits of a call alone."""
+    f = Ffn(20, 512, 256, 12, 3, True, seed=41)
+    f.run()
+    torch.cuda.synchronize()
+    want = f.y.clone()
+    f.check()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(4)]
+    for i in range(8):
+        f.buffers()
+        outs.append((f.h, f.hs, f.y, f.err))
+    torch.cuda.synchronize()
+    for i, (f.h, f.hs, f.y, f.err) in enumerate(outs):
+        f.run(streams[i % 4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[2], want) and o[3].item() == 0 for o in outs)
 
 
 def test_other_devices_and_host_outputs_are_refused():
