@@ -116,7 +116,8 @@ int ft_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long
   const char* call = "ft_rmsnorm_fp8";
   if (!(eps >= 0.0f)) return bad(call, "eps must be a number of at least 0");
   if (T > 0 && !weight) return bad(call, "null pointer");
-  const ftk::RowsFp8 p{x, residual, weight, residual_out, y, static_cast<uint8_t*>(q), scales, ldx, ldr, ldq, T, H, eps};
+  const ftk::RowsFp8 p{x,   residual, weight, residual_out, y, static_cast<uint8_t*>(q), scales,
+                       ldx, ldr,      ldq,    T,            H, eps};
   return rows_call(call, p, x_is_bf16, stream);
 }
 

@@ -34,6 +34,7 @@
 // three quarters of the multiply-adds (600), and two buffers of 256 columns fill TMEM.  Tried and
 // slower: halves of N = 128 with two buffers each (the shared-memory reads of A double), 16
 // summing warps (spills), two CTAs per SM with 128 x 128 tiles, paired multiply-adds (moves).
+//
 // gate/up tiles hold 128 gate and 128 up columns; each half of the warps takes 64 columns of
 // both, so silu(gate) * up stays inside a thread.
 //
@@ -205,7 +206,8 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       int it = 0;
       for (long long left = (long long)mine * KB; left > 0; --left, ++it) {
         const int s = it % STAGES, b = it & 1;
-        if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122)) break;
+        if (!warp_wait2(&S->full[s], (it / STAGES) & 1, &S->tempty[b], ((it >> 1) & 1) ^ 1, abort_flag, err, 122))
+          break;
         fp8_fence_after();
         if (elect_one()) {
           const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4)), db = da + (A_BYTES >> 4);
@@ -234,8 +236,10 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         const long long wz = groups.z[g] * p.blob;
         const float* sw[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)(MODE == 0 ? n : min(2 * n + i, NB - 1)) * KB;
+        for (int i = 0; i < 2; ++i) {
+          const int nb = MODE == 0 ? n : min(2 * n + i, NB - 1);
+          sw[i] = reinterpret_cast<const float*>(p.w_scales[i] + wz) + (long long)nb * KB;
+        }
         bool ok = true;
         for (int k0 = 0; k0 < KB; k0 += FK, ++ch) {
           const int b = ch & 1;
@@ -435,9 +439,9 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
 
 // The token row of every listed pair, H bytes (a multiple of 16) at dst + pair * stride.
 // One warp per row; bound by memory (the reads hit the L2).
-__global__ void __launch_bounds__(256) fp8_gather_kernel(const uint8_t* x, long long ldx, const __grid_constant__ GemmGroups groups,
-                                                         const int* offsets, const int* perm, int T, int k, int H,
-                                                         uint8_t* dst, long long stride) {
+__global__ void __launch_bounds__(256)
+fp8_gather_kernel(const uint8_t* x, long long ldx, const __grid_constant__ GemmGroups groups, const int* offsets,
+                  const int* perm, int T, int k, int H, uint8_t* dst, long long stride) {
   const int g = blockIdx.y, e = groups.expert[g], lane = threadIdx.x & 31;
   const int first = e >= 0 ? offsets[e] : T * k, last = e >= 0 ? offsets[e + 1] : T * k + T;
   for (int q = first + blockIdx.x * 8 + (threadIdx.x >> 5); q < last; q += gridDim.x * 8) {

@@ -182,7 +182,8 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         }
         __syncwarp();
         if (MODE == 0 && lane < NT / 4)
-          fp8_tma_gather4(sw + W * WTILE + lane * 4 * BK, &maps.a, &S->full[s], kb * BK, tok[0], tok[1], tok[2], tok[3]);
+          fp8_tma_gather4(sw + W * WTILE + lane * 4 * BK, &maps.a, &S->full[s], kb * BK, tok[0], tok[1], tok[2],
+                          tok[3]);
         __syncwarp();
       }
       // drain: wait (bounded) until every issued stage has landed
