@@ -617,6 +617,24 @@ FT_API int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales
                              const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
                              void* stream);
 
+/* The fp8 products run in one of several forms, chosen by an estimate of time from the sizes.  A plan
+ * is three ints: tokens per CTA (16, 32; gate/up 64, product 128) of the kernel that streams the
+ * weights, or 0 for the 128 x 256 tiles; parts of K (1, 2, 4, 8; at most its blocks of 128); CTAs
+ * (1 .. 64) that share an expert's tokens.  The last two count for the streaming kernel only.
+ *   ft_debug_fp8_plan: the plan of a product of N columns and K over `groups` experts of `rows` rows each
+ *     (ft_gemm_fp8: one group, rows_aligned = rows of out at 16-byte addresses) on num_sms SMs; mode 0:
+ *     gate/up (N = I, K = H), 1: the product.  Needs no device.
+ *   ft_debug_gemm_fp8, ft_debug_expert_ffn_fp8: the calls without `debug`, by the caller's plan (for the
+ *     FFN: gate/up's, then down's).  The results differ by the order of the f32 sums only. */
+FT_API int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms, int rows_aligned, int* plan3);
+FT_API int ft_debug_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
+                             const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo,
+                             int* err, const int* plan3, void* stream);
+FT_API int ft_debug_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
+                                   const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
+                                   const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
+                                   const int* plan6, void* stream);
+
 /* Version string of the library build. */
 FT_API const char* ft_version(void);
 

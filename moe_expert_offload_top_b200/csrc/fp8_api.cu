@@ -88,6 +88,13 @@ Plan plan(int mode, long long rows, int groups, int N, int K, int sms, bool alig
   }
   return best;
 }
+// A plan that the kernels can run: the token counts of `mode`, K in 1, 2, 4 or 8 parts of a block at least.
+bool valid(int mode, const Plan& p, int K) {
+  if (p.nt == 0) return true;
+  if (p.nt != 16 && p.nt != 32 && p.nt != (mode == 0 ? 64 : 128)) return false;
+  if (p.split < 1 || p.split > 8 || (p.split & (p.split - 1)) || p.split > ftk::fp8_blocks(K)) return false;
+  return p.chunks >= 1 && p.chunks <= 64;
+}
 
 int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stream) {
   const uintptr_t es = x_is_bf16 ? 2 : 4;
@@ -106,35 +113,14 @@ int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stre
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
 
-}  // namespace
-
-extern "C" {
-
-int ft_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* weight,
-                   int x_is_bf16, int T, int H, float eps, void* residual_out, void* y, void* q, long long ldq,
-                   float* scales, void* stream) {
-  const char* call = "ft_rmsnorm_fp8";
-  if (!(eps >= 0.0f)) return bad(call, "eps must be a number of at least 0");
-  if (T > 0 && !weight) return bad(call, "null pointer");
-  const ftk::RowsFp8 p{x,   residual, weight, residual_out, y, static_cast<uint8_t*>(q), scales,
-                       ldx, ldr,      ldq,    T,            H, eps};
-  return rows_call(call, p, x_is_bf16, stream);
-}
-
-int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, int H, void* q, long long ldq, float* scales,
-                    void* stream) {
-  if (T > 0 && !q) return bad("ft_quantize_fp8", "null pointer");
-  const ftk::RowsFp8 p{x, nullptr, nullptr, nullptr, nullptr, static_cast<uint8_t*>(q), scales, ldx, 0, ldq, T, H, 0.f};
-  return rows_call("ft_quantize_fp8", p, x_is_bf16, stream);
-}
-
-int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
-                const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
-                void* stream) {
-  const char* call = "ft_gemm_fp8";
+// ft_gemm_fp8, by `forced` where that is given.
+int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
+             const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
+             const Plan* forced, void* stream) {
   if (M < 0 || N < 0 || K < 1) return bad(call, "invalid size");
   if (lda < K || ldw < K || ldo < N) return bad(call, "a row stride is smaller than the row");
   if (lda % 16 || ldw % 16) return bad(call, "lda and ldw must be multiples of 16");
+  if (forced && !valid(1, *forced, K)) return bad(call, "no such plan");
   if (M == 0 || N == 0) return FT_OK;
   if (!a || !a_scales || !w || !w_scales || !out || !err) return bad(call, "null pointer");
   if (!aligned(a, 16) || !aligned(w, 16)) return bad(call, "a and w must be 16-byte aligned");
@@ -143,7 +129,8 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
   const int rc = check_device(call, out);
   if (rc != FT_OK) return rc;
   const int sms = num_sms();
-  const Plan pl = plan(1, M, 1, N, K, sms, ldo * (out_is_bf16 ? 2 : 4) % 16 == 0 && aligned(out, 16));
+  const Plan pl =
+      forced ? *forced : plan(1, M, 1, N, K, sms, ldo * (out_is_bf16 ? 2 : 4) % 16 == 0 && aligned(out, 16));
   ftk::Fp8Maps m;
   if (!ftk::encode_map_fp8(&m.a, a, K, M, lda, 0, 0, pl.nt ? pl.nt : 128) ||
       !ftk::encode_map_fp8(&m.b[0], w, K, N, ldw, 1, (uint64_t)ldw * N, 128)) {
@@ -163,22 +150,17 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
 
-size_t ft_fp8_blob_bytes(int H, int I) {
-  if (H < 16 || I < 16 || H % 16 || I % 16) return 0;
-  const size_t scales = (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
-  return (3 * ((size_t)H * I + 4 * scales) + 15) / 16 * 16;
-}
-
-int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
-                      const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
-                      const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
-                      void* stream) {
-  const char* call = "ft_expert_ffn_fp8";
+// ft_expert_ffn_fp8; by forced[0] (gate/up) and forced[1] (down) where that is given.
+int expert_ffn_fp8(const char* call, const void* x, long long ldx, const float* x_scales, int T, int H, int I,
+                   int top_k, const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
+                   const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
+                   const Plan* forced, void* stream) {
   if (T < 0 || top_k < 1 || top_k > FT_MAX_TOPK || n_list < 0 || n_list > ftk::kMaxList || n_slots < 1)
     return bad(call, "invalid size");
   if (H < 16 || I < 16 || H % 16 || I % 16) return bad(call, "H and I must be multiples of 16");
   if ((long long)T * (top_k + 1) > 0x7FFFFFFF) return bad(call, "T * (top_k + 1) is above 2^31 - 1");
   if (ldx < H || ldx % 16) return bad(call, "ldx must be a multiple of 16 of at least H");
+  if (forced && (!valid(0, forced[0], H) || !valid(1, forced[1], I))) return bad(call, "no such plan");
   if (T == 0 || n_list == 0) return FT_OK;
   if (!x || !x_scales || !weights || !experts || !slots || !offsets || !perm || !h || !h_scales || !y || !err)
     return bad(call, "null pointer");
@@ -212,7 +194,7 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   // the pairs' token rows in the rows of y that the down product writes last.
   const char* what = "launch: ";
   auto product = [&](int mode, const ftk::GemmGroups& gr, long long rows, bool early) -> cudaError_t {
-    const Plan pl = plan(mode, rows, gr.n, mode == 0 ? I : H, mode == 0 ? H : I, sms, true);
+    const Plan pl = forced ? forced[mode] : plan(mode, rows, gr.n, mode == 0 ? I : H, mode == 0 ? H : I, sms, true);
     const uint32_t box = pl.nt ? pl.nt : 128;
     ftk::Fp8Maps m;
     bool ok;
@@ -241,7 +223,7 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
   const double even = routed ? (double)T * top_k / routed : 0.0;
   const long long each = std::min((long long)T, (long long)std::ceil(even + 3.0 * std::sqrt(even)));
   cudaError_t e;
-  if (seen[0] && routed && T > 16 && T > 2 * each && plan(0, each, routed, I, H, sms, true).nt) {
+  if (!forced && seen[0] && routed && T > 16 && T > 2 * each && plan(0, each, routed, I, H, sms, true).nt) {
     // far more rows in the shared expert, and the others stream: its products are launched by
     // themselves (100 tokens, 64 experts, top 4: 342 -> 279 us); the tiles take any mix at once
     ftk::GemmGroups some, shared;
@@ -263,6 +245,78 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
     if (e == cudaSuccess) e = product(1, groups, rows, true);
   }
   return e == cudaSuccess ? FT_OK : failed(call, what, e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ft_rmsnorm_fp8(const void* x, long long ldx, const void* residual, long long ldr, const void* weight,
+                   int x_is_bf16, int T, int H, float eps, void* residual_out, void* y, void* q, long long ldq,
+                   float* scales, void* stream) {
+  const char* call = "ft_rmsnorm_fp8";
+  if (!(eps >= 0.0f)) return bad(call, "eps must be a number of at least 0");
+  if (T > 0 && !weight) return bad(call, "null pointer");
+  const ftk::RowsFp8 p{x,   residual, weight, residual_out, y, static_cast<uint8_t*>(q), scales,
+                       ldx, ldr,      ldq,    T,            H, eps};
+  return rows_call(call, p, x_is_bf16, stream);
+}
+
+int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, int H, void* q, long long ldq, float* scales,
+                    void* stream) {
+  if (T > 0 && !q) return bad("ft_quantize_fp8", "null pointer");
+  const ftk::RowsFp8 p{x, nullptr, nullptr, nullptr, nullptr, static_cast<uint8_t*>(q), scales, ldx, 0, ldq, T, H, 0.f};
+  return rows_call("ft_quantize_fp8", p, x_is_bf16, stream);
+}
+
+int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
+                const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
+                void* stream) {
+  return gemm_fp8("ft_gemm_fp8", a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, nullptr,
+                  stream);
+}
+
+size_t ft_fp8_blob_bytes(int H, int I) {
+  if (H < 16 || I < 16 || H % 16 || I % 16) return 0;
+  const size_t scales = (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
+  return (3 * ((size_t)H * I + 4 * scales) + 15) / 16 * 16;
+}
+
+int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
+                      const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
+                      const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
+                      void* stream) {
+  return expert_ffn_fp8("ft_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, n_list,
+                        offsets, perm, h, h_scales, y, err, nullptr, stream);
+}
+
+int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms, int rows_aligned, int* plan3) {
+  if ((mode != 0 && mode != 1) || rows < 0 || groups < 1 || N < 1 || K < 1 || num_sms < 1 || !plan3)
+    return bad("ft_debug_fp8_plan", "invalid argument");
+  const Plan p = plan(mode, rows, groups, N, K, num_sms, rows_aligned != 0);
+  plan3[0] = p.nt;
+  plan3[1] = p.split;
+  plan3[2] = p.chunks;
+  return FT_OK;
+}
+
+int ft_debug_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
+                      const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
+                      const int* plan3, void* stream) {
+  if (!plan3) return bad("ft_debug_gemm_fp8", "null pointer");
+  const Plan p{plan3[0], plan3[1], plan3[2]};
+  return gemm_fp8("ft_debug_gemm_fp8", a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, &p,
+                  stream);
+}
+
+int ft_debug_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
+                            const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
+                            const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
+                            const int* plan6, void* stream) {
+  if (!plan6) return bad("ft_debug_expert_ffn_fp8", "null pointer");
+  const Plan p[2] = {{plan6[0], plan6[1], plan6[2]}, {plan6[3], plan6[4], plan6[5]}};
+  return expert_ffn_fp8("ft_debug_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots,
+                        n_list, offsets, perm, h, h_scales, y, err, p, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,53 @@
+"""How the fp8 products choose their form, and the refusals of forced plans (no GPU)."""
+import pytest
+
+import moe_expert_offload_top_b200 as ft
+from test_fp8_cpu import FFN, GEMM, _refused
+
+
+@pytest.mark.parametrize("mode,rows,groups,N,K,want", [
+    (1, 1, 1, 4096, 4096, (16, 4)), (1, 32, 1, 7168, 2048, (32, 2)), (1, 300, 1, 2048, 2048, (128, 2)),
+    (1, 8192, 1, 7168, 4096, (0, 1)), (0, 1, 7, 2048, 4096, (16, 1)), (0, 4096, 1, 128, 1024, (64, 2)),
+    (0, 4096, 64, 2048, 4096, (0, 1))])
+def test_plan_of_ordinary_sizes(mode, rows, groups, N, K, want):
+    nt, split, chunks = ft.ft_debug_fp8_plan(mode, rows, groups, N, K)
+    assert (nt, split) == want
+    assert chunks == (1 if nt == 0 else -(-rows // nt))
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+def test_every_plan_is_one_that_the_kernels_take(mode):
+    for rows in (1, 3, 16, 17, 33, 65, 129, 300, 1000, 5000, 70000):
+        for N in (1, 16, 129, 500, 2048, 8192):
+            for K in (1, 16, 129, 300, 1000, 4096):
+                nt, split, chunks = ft.ft_debug_fp8_plan(mode, rows, 5, N, K)
+                assert nt in ((0, 16, 32, 64) if mode == 0 else (0, 16, 32, 128))
+                assert split in (1, 2, 4, 8) and split <= -(-K // 128) and 1 <= chunks <= 64
+                assert nt == 0 or nt * chunks >= rows
+
+
+@pytest.mark.parametrize("args", [(2, 1, 1, 1, 1), (0, -1, 1, 1, 1), (0, 1, 0, 1, 1), (0, 1, 1, 0, 1), (0, 1, 1, 1, 0),
+                                  (0, 1, 1, 1, 1, 0)])
+def test_plan_refusals(args):
+    with pytest.raises(ft.FtError) as e:
+        ft.ft_debug_fp8_plan(*args)
+    assert "ft_debug_fp8_plan" in str(e.value)
+
+
+@pytest.mark.parametrize("plan", [(64, 1, 1), (8, 1, 1), (-16, 1, 1), (16, 0, 1), (16, 3, 1), (16, 4, 1), (16, 16, 1),
+                                  (16, 1, 0), (16, 1, 65)])
+def test_forced_plans_are_checked(plan):
+    _refused(ft.ft_debug_gemm_fp8, dict(GEMM, plan=plan), {}, "plan")        # K = 250: two blocks
+    _refused(ft.ft_debug_expert_ffn_fp8, dict(FFN, gate_up=(0, 1, 1), down=plan), {}, "plan")
+    gate_up = (128, *plan[1:]) if plan[0] == 64 else plan
+    _refused(ft.ft_debug_expert_ffn_fp8, dict(FFN, gate_up=gate_up, down=(0, 1, 1)), {}, "plan")
+
+
+@pytest.mark.parametrize("change,word", [(dict(lda=240), "stride"), (dict(a=None), "null"), (dict(out=7), "aligned")])
+def test_forced_calls_check_their_arguments(change, word):
+    _refused(ft.ft_debug_gemm_fp8, dict(GEMM, plan=(0, 1, 1)), change, word)
+
+
+def test_forced_empty_calls_do_nothing():
+    ft.ft_debug_gemm_fp8(*dict(GEMM, M=0, plan=(0, 1, 1)).values())
+    ft.ft_debug_expert_ffn_fp8(*dict(FFN, T=0, gate_up=(0, 1, 1), down=(0, 1, 1)).values())

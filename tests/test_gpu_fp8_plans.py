@@ -1,0 +1,256 @@
+"""Every form of the fp8 products against the float64 oracle, whatever the estimate of time would
+pick: the 128 x 256 tiles and each streaming kernel (tokens per CTA x parts of K x CTAs per
+expert), forced by the ft_debug_* entries, at odd sizes, partial blocks, NaN codes, lists with
+empty and unlisted experts, on several streams and captured; and the public calls at sizes
+whose plan is asserted.
+
+Tolerances are those of fp8.product_bound: parts of K added over the cluster take the place of
+as many steps of the chain over blocks, so the roundings counted there are not exceeded."""
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_offload_top_b200 as ft
+from oracle import fp8
+from test_gpu_fp8 import DEV, UBF, Ffn, _bytes, _dt, _err, _np, _operand, _scales
+
+pytestmark = pytest.mark.gpu
+
+TILES = (0, 1, 1)
+PRODUCT = [TILES] + [(nt, split, chunks) for nt in (16, 32, 128) for split, chunks in ((1, 3), (2, 1), (4, 2), (8, 1))]
+GATE_UP = [TILES] + [(nt, split, chunks) for nt in (16, 32, 64) for split, chunks in ((1, 2), (2, 1), (4, 3), (8, 1))]
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _gemm_case(M, N, K, seed, pad=0):
+    gen = torch.Generator().manual_seed(seed)
+    ld = -(-K // 16) * 16 + pad
+    a, w = _operand(M, K, ld, gen), _operand(N, K, ld, gen)
+    sa, sw = _scales((M, fp8.blocks(K)), gen), _scales((fp8.blocks(N), fp8.blocks(K)), gen)
+    return ld, a, w, sa, sw
+
+
+def _check_product(out, a, sa, w, sw, K, bf16):
+    ref, l1 = fp8.product(fp8.decode(_bytes(a)[:, :K]), _np(sa), fp8.decode(_bytes(w)[:, :K]), _np(sw))
+    tol = fp8.product_bound(l1, K) + (UBF * np.abs(ref) * (1 + UBF) if bf16 else 0.0)
+    off = np.abs(_np(out) - ref)
+    assert (off <= tol).all(), np.max(off / tol)
+
+
+# K = 1133: eight whole blocks of K and a ninth that ends inside; 1250: more than one chunk of factors
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,N,K,ldo", [
+    (1, 130, 1133, 131),        # one row, rows of out that no wide store fits
+    (150, 300, 1250, 304),      # 16-byte rows of out, a ragged last column
+    (150, 300, 1250, 320),      # 32-byte rows
+    (261, 515, 1024, 517),      # several tiles, odd rows
+    (40, 264, 2000, 264)])
+@pytest.mark.parametrize("plan", PRODUCT)
+def test_gemm_by_plan(plan, M, N, K, ldo, bf16):
+    ld, a, w, sa, sw = _gemm_case(M, N, K, M + N + K, pad=16)
+    out, err = torch.full((M + 1, ldo), 77.0, dtype=_dt(bf16), device=DEV), _err()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, bf16, out, ldo, err, plan)
+    assert err.item() == 0
+    _check_product(out[:M, :N], a, sa, w, sw, K, bf16)
+    assert (out[M] == 77).all() and (out[:, N:] == 77).all()
+
+
+@pytest.mark.parametrize("plan", [p for p in PRODUCT if p[1] <= 2])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 129), (3, 17, 200), (129, 257, 255)])
+def test_gemm_by_plan_two_blocks(plan, M, N, K):
+    """As few blocks of K as the plan allows: each part has one at most."""
+    ld, a, w, sa, sw = _gemm_case(M, N, K, 3)
+    out, err = torch.zeros((M, N), device=DEV), _err()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, plan)
+    assert err.item() == 0
+    _check_product(out, a, sa, w, sw, K, False)
+
+
+@pytest.mark.parametrize("plan", PRODUCT)
+def test_gemm_by_plan_nan_codes_and_zero_rows(plan):
+    """A NaN code reaches its row or column and nothing else; rows of zeros and zero scales give zeros."""
+    M, N, K = 140, 300, 1100
+    ld, a, w, sa, sw = _gemm_case(M, N, K, 1)
+    a[5] = 0
+    a[130, 17] = 0x7F
+    w[299, 1080] = 0xFF
+    sa[6] = 0.0
+    out, err = torch.zeros((M, N), device=DEV), _err()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, plan)
+    assert err.item() == 0
+    want = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    want[:, 299] = True
+    want[130] = True
+    assert torch.equal(torch.isnan(out), want)
+    assert (out[5, :299] == 0).all() and (out[6, :299] == 0).all()
+
+
+@pytest.mark.parametrize("plan", [TILES, (16, 1, 2), (32, 4, 1), (128, 2, 1), (128, 8, 1)])
+def test_gemm_by_plan_streams_repeats_and_graph(plan):
+    """The same call on four streams at once, again, and captured gives the same bits."""
+    M, N, K = 260, 1000, 2048
+    ld, a, w, sa, sw = _gemm_case(M, N, K, 2)
+    first, err = torch.zeros((M, N), device=DEV), _err()
+
+    def call(out, stream=None):
+        ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, plan, stream)
+    call(first)
+    torch.cuda.synchronize()
+    outs = [torch.zeros((M, N), device=DEV) for _ in range(8)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        call(o, streams[i % 4])
+    torch.cuda.synchronize()
+    assert err.item() == 0 and all(torch.equal(o, first) for o in outs)
+    graph, out = torch.cuda.CUDAGraph(), outs[0]
+    with torch.cuda.graph(graph, stream=streams[0]):
+        call(out, streams[0])
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    assert err.item() == 0
+
+
+# ------------------------------------------------- expert FFN, by plan --
+
+class PlannedFfn(Ffn):
+    plans = (TILES, TILES)
+
+    def run(self, stream=None, experts=None, slots=None):
+        ft.ft_debug_expert_ffn_fp8(self.x, self.ldx, self.xs, self.T, self.H, self.I, self.k, self.weights, self.n_slots,
+                                   self.experts if experts is None else experts, self.slots if slots is None else slots,
+                                   self.offsets, self.perm, self.h, self.hs, self.y, self.err, *self.plans, stream)
+
+
+# every gate/up form, each with another form of the down product
+PAIRS = [(g, PRODUCT[(5 * i + 1) % len(PRODUCT)]) for i, g in enumerate(GATE_UP)] + [(TILES, TILES), ((64, 2, 1), TILES)]
+
+
+@pytest.mark.parametrize("gate_up,down", PAIRS)
+@pytest.mark.parametrize("T,H,I,E,k,shared,empty,skew", [
+    (1, 1040, 1040, 4, 2, True, (), 0.0),            # H and I end inside their last block; one token
+    (75, 912, 928, 5, 2, True, (0, 4), 1.0),       # experts without tokens first and last in the list
+    (140, 1024, 1024, 3, 1, False, (), 2.0)])
+def test_expert_ffn_by_plan(gate_up, down, T, H, I, E, k, shared, empty, skew):
+    f = PlannedFfn(T, H, I, E, k, shared, seed=T + H, empty=empty, skew=skew, pad=16 * (T % 2))
+    f.plans = gate_up, down
+    f.run()
+    f.check()
+
+
+@pytest.mark.parametrize("plan", [TILES, (16, 2, 1), (32, 1, 1), (64, 1, 2)])
+def test_expert_ffn_by_plan_unlisted_experts(plan):
+    f = PlannedFfn(90, 272, 400, 6, 3, True, seed=5)
+    f.plans = plan, (128 if plan[0] == 64 else plan[0], *plan[1:])
+    drop = {1, 4, -1}
+    keep = [(e, s) for e, s in zip(f.experts, f.slots) if e not in drop]
+    f.run(experts=[e for e, _ in keep], slots=[s for _, s in keep])
+    f.check(skip=drop)
+
+
+@pytest.mark.parametrize("plan", [TILES, (64, 1, 1), (32, 2, 2)])
+def test_expert_ffn_by_plan_streams_and_graph(plan):
+    f = PlannedFfn(130, 400, 272, 5, 2, True, seed=41)
+    f.plans = plan, (128 if plan[0] == 64 else plan[0], *plan[1:])
+    f.run()
+    torch.cuda.synchronize()
+    want = f.y.clone()
+    f.check()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(4)]
+    for i in range(8):
+        f.buffers()
+        outs.append((f.h, f.hs, f.y, f.err))
+    torch.cuda.synchronize()
+    for i, (f.h, f.hs, f.y, f.err) in enumerate(outs):
+        f.run(streams[i % 4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[2], want) and o[3].item() == 0 for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        f.run(streams[0])
+    f.y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(f.y, want) and f.err.item() == 0
+
+
+# ---------------------------------------------- public calls, plan asserted --
+
+@pytest.mark.parametrize("M,N,K,bf16,nt,split", [
+    (700, 8200, 1133, True, 0, 1),      # tiles, a ragged K
+    (1030, 8101, 1250, False, 0, 1),     # tiles, odd rows of out
+    (200, 768, 2048, True, 32, 2), (160, 520, 1100, False, 32, 4), (300, 2048, 2048, True, 128, 2),
+    (300, 1030, 4000, False, 128, 4), (300, 512, 7100, True, 128, 8), (2, 7168, 2000, False, 16, 2)])
+def test_gemm_at_sizes_of_each_plan(M, N, K, bf16, nt, split):
+    aligned = N * (2 if bf16 else 4) % 16 == 0
+    assert ft.ft_debug_fp8_plan(1, M, 1, N, K, _sms(), aligned)[:2] == (nt, split)
+    ld, a, w, sa, sw = _gemm_case(M, N, K, N)
+    out, err = torch.zeros((M, N), dtype=_dt(bf16), device=DEV), _err()
+    ft.ft_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, bf16, out, N, err)
+    assert err.item() == 0
+    rows = [0, 1, M // 2, M - 2, M - 1]      # the whole is compared with the tiles' own check above
+    _check_product(out[rows], a[rows], sa[rows], w, sw, K, bf16)
+    forced = torch.zeros_like(out)
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, bf16, forced, N, err,
+                         ft.ft_debug_fp8_plan(1, M, 1, N, K, _sms(), aligned))
+    assert torch.equal(forced, out)
+
+
+@pytest.mark.parametrize("T,H,I,E,k,nt", [(900, 528, 400, 3, 2, 0), (1000, 1040, 272, 4, 2, 0)])
+def test_expert_ffn_at_sizes_of_the_tiles(T, H, I, E, k, nt):
+    even = T * k / E
+    rows = max(min(T, int(np.ceil(even + 3 * np.sqrt(even)))), T)
+    assert ft.ft_debug_fp8_plan(0, rows, E + 1, I, H, _sms())[0] == nt
+    f = Ffn(T, H, I, E, k, True, seed=T, empty=(1,), skew=0.5)
+    f.run()
+    f.check()
+
+
+# -------------------------------------------------------------- norm, rows --
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,H", [(297, 4112), (300, 7168), (400, 9008), (299, 16384)])
+def test_rmsnorm_many_wide_aligned_rows(T, H, bf16):
+    """Two chunks per thread: more than 296 aligned rows wider than 4096."""
+    from test_gpu_fp8 import EPS, _norm_bound, check_codes
+    g = torch.Generator().manual_seed(H)
+    x, res = ((torch.randn((T, H + 16), generator=g) * s).to(_dt(bf16)).to(DEV) for s in (2, 5))
+    w = (1 + 0.3 * torch.randn(H, generator=g)).to(_dt(bf16)).to(DEV)
+    y = torch.full((T + 1, H), 77.0, dtype=_dt(bf16), device=DEV)
+    r = torch.full((T + 1, H + 16), 77.0, dtype=_dt(bf16), device=DEV)
+    q = torch.full((T + 1, H + 16), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((T + 1, fp8.blocks(H)), -1.0, device=DEV)
+    ft.ft_rmsnorm_fp8(x, H + 16, res, H + 16, w, bf16, T, H, EPS, r, y, q, H + 16, s)
+    want = (x[:, :H].float() + res[:, :H].float()).to(_dt(bf16))
+    assert torch.equal(r[:T, :H], want) and (r[T] == 77).all() and (r[:, H:] == 77).all()
+    assert (y[T] == 77).all() and (q[T] == 0x55).all() and (q[:, H:] == 0x55).all() and (s[T] == -1).all()
+    ref = fp8.rmsnorm(_np(want), _np(w), EPS)
+    rel = _norm_bound(H)
+    assert (np.abs(_np(y[:T]) - ref) <= (rel + (UBF if bf16 else 0.0)) * np.abs(ref) * (1 + UBF) + 1e-38).all()
+    check_codes(_bytes(q[:T, :H]), _np(s[:T]), ref, rel)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,H", [(32, 7168), (300, 4096), (33, 2051), (5, 200)])
+def test_quantised_rows_are_the_formula_bit_for_bit(T, H, bf16):
+    """s = max(max |y| / 448, 2^-126) rounded once, q = e4m3(y * (1 / s)) with the inverse and the product
+    rounded once each: three IEEE operations, so the bits are known."""
+    g = torch.Generator().manual_seed(T + H)
+    x = (torch.randn((T, H), generator=g) * torch.exp2(torch.randint(-20, 20, (T, 1), generator=g).float())).to(_dt(bf16))
+    pad = torch.zeros((T, fp8.blocks(H) * 128))
+    pad[:, :H] = x.float()
+    b = pad.numpy().reshape(T, -1, 128)
+    scale = np.maximum(np.abs(b).max(2) / np.float32(448), np.float32(2.0 ** -126))
+    assert scale.dtype == np.float32
+    v = (b * (np.float32(1) / scale)[..., None]).reshape(T, -1)[:, :H]
+    assert v.dtype == np.float32
+    q, s = torch.zeros((T, H), dtype=torch.uint8, device=DEV), torch.zeros((T, fp8.blocks(H)), device=DEV)
+    ft.ft_quantize_fp8(x.to(DEV), H, bf16, T, H, q, H, s)
+    assert np.array_equal(s.cpu().numpy(), scale)
+    assert np.array_equal(fp8.decode(_bytes(q)), fp8.round_e4m3(v))
