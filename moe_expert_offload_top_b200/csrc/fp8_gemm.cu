@@ -286,8 +286,9 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       float acc[HN];
 #pragma unroll
       for (int i = 0; i < HN; ++i) acc[i] = 0.f;
-      // The next block's first columns are asked for before this one's last are added, so that
-      // the wait for the tensor cores and the load's latency pass behind multiply-adds.
+      // The next columns are asked for before these are added, the next block's first before
+      // this one's last, so that the wait for the tensor cores and the load's latency pass behind
+      // multiply-adds.  No load is pending where the loop turns (tmem_wait).
       uint32_t v[2][LC];
       auto ready = [&](int i) {   // accumulators of block i (over the tiles)
         const bool w = warp_wait(&S->done[i % STAGES], (i / STAGES) & 1, abort_flag, err, 123);
@@ -297,6 +298,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       bool ok = ready(it);
       if (!ok) break;
       tmem_ld(col0 + (it & 1) * BN, v[0]);
+      tmem_wait(v[0]);
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int b = it & 1, j = kb % FK, fb = ch & 1;
         if (j == 0) {
@@ -307,7 +309,6 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         const float f0 = S->factor[fb][j][MODE == 0 ? 0 : half][r], f1 = MODE == 0 ? S->factor[fb][j][1][r] : f0;
 #pragma unroll
         for (int c = 0; c < NL; ++c) {
-          tmem_wait();
           if (c + 1 < NL) {
             tmem_ld(ta + column(c + 1), v[(c + 1) & 1]);
           } else {
@@ -324,6 +325,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
           }
 #pragma unroll
           for (int i = 0; i < LC; ++i) fma_col(acc[LC * c + i], v[c & 1][i], MODE == 0 && c >= NL / 2 ? f1 : f0);
+          tmem_wait(v[(c + 1) & 1]);
         }
         if (!ok) break;
       }

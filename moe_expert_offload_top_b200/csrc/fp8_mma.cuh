@@ -81,7 +81,9 @@ FT_DEVICE void fp8_commit(uint64_t* bar) {
 FT_DEVICE void fp8_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 FT_DEVICE void fp8_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 or 32 accumulator columns of this thread's TMEM lane; tmem_wait before the values are used.
+// 16 or 32 accumulator columns of this thread's TMEM lane.  The registers hold nothing before
+// tmem_wait on them, which therefore has to follow in the same pass of a loop: a copy that the
+// compiler places between the two (at a loop's back edge, say) would read them too early.
 FT_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -102,7 +104,23 @@ FT_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-FT_DEVICE void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads so far have landed, r's among them: r passes through, so that its uses stay behind.
+FT_DEVICE void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+               "+r"(r[15])
+               :: "memory");
+}
+FT_DEVICE void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+               "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+               "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+               "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
 
 // acc += v * s, rounded once.  volatile: stays behind the wait for the accumulator column v.
 FT_DEVICE void fma_col(float& acc, uint32_t v, float s) {

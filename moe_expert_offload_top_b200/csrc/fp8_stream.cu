@@ -266,7 +266,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         for (int j = 0; j < CHUNKS; ++j) {
           uint32_t v[16];
           tmem_ld(lane_base + b * COLS + column(j), v);
-          tmem_wait();
+          tmem_wait(v);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float4 x = *reinterpret_cast<const float4*>(&S->factor[fb][f][column(j) + 4 * y]);
