@@ -625,15 +625,18 @@ FT_API int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales
  *     (ft_gemm_fp8: one group, rows_aligned = rows of out at 16-byte addresses) on num_sms SMs; mode 0:
  *     gate/up (N = I, K = H), 1: the product.  Needs no device.
  *   ft_debug_gemm_fp8, ft_debug_expert_ffn_fp8: the calls without `debug`, by the caller's plan (for the
- *     FFN: gate/up's, then down's).  The results differ by the order of the f32 sums only. */
+ *     FFN: gate/up's, then down's).  The results differ by the order of the f32 sums only.  fail_at
+ *     (-1: nowhere): in each CTA's chunk of tokens, or tile, of that number a device wait runs for 1 ms on
+ *     a barrier that nothing arrives on and gives up: 129 or 121 in *err, that chunk or tile and the
+ *     CTA's later ones are left unwritten, and the kernel returns. */
 FT_API int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms, int rows_aligned, int* plan3);
 FT_API int ft_debug_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
                              const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo,
-                             int* err, const int* plan3, void* stream);
+                             int* err, const int* plan3, int fail_at, void* stream);
 FT_API int ft_debug_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
                                    const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
                                    const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
-                                   const int* plan6, void* stream);
+                                   const int* plan6, int fail_at, void* stream);
 
 /* Version string of the library build. */
 FT_API const char* ft_version(void);

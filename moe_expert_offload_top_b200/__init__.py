@@ -103,9 +103,9 @@ _SIGS = {
     "ft_expert_ffn_fp8": ([_vp, _ll, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
                           _i),
     "ft_debug_fp8_plan": ([_i, _i, _i, _i, _i, _i, _i, _vp], _i),
-    "ft_debug_gemm_fp8": ([_vp, _ll, _vp, _vp, _ll, _vp, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _vp], _i),
+    "ft_debug_gemm_fp8": ([_vp, _ll, _vp, _vp, _ll, _vp, _i, _i, _i, _i, _vp, _ll, _vp, _vp, _i, _vp], _i),
     "ft_debug_expert_ffn_fp8": ([_vp, _ll, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
-                                 _vp, _vp], _i),
+                                 _vp, _i, _vp], _i),
     "ft_version": ([], ctypes.c_char_p),
     "ft_moe_set_stage_timing": ([_vp, _i], _i),
     "ft_moe_sync": ([_vp], _i),
@@ -399,16 +399,19 @@ def ft_debug_fp8_plan(mode, rows, groups, N, K, num_sms=148, rows_aligned=True):
     return tuple(out)
 
 
-def ft_debug_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, plan, stream=None):
+def ft_debug_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, plan, fail_at=-1,
+                      stream=None):
     return _check(None, _lib.ft_debug_gemm_fp8(_p(a), lda, _p(a_scales), _p(w), ldw, _p(w_scales), M, N, K,
-                                               int(out_is_bf16), _p(out), ldo, _p(err), _int_array(_plan3(plan)), _s(stream)))
+                                               int(out_is_bf16), _p(out), ldo, _p(err), _int_array(_plan3(plan)), fail_at,
+                                               _s(stream)))
 
 
 def ft_debug_expert_ffn_fp8(x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets, perm, h,
-                            h_scales, y, err, gate_up_plan, down_plan, stream=None):
+                            h_scales, y, err, gate_up_plan, down_plan, fail_at=-1, stream=None):
     return _check(None, _lib.ft_debug_expert_ffn_fp8(
         _p(x), ldx, _p(x_scales), T, H, I, top_k, _p(weights), n_slots, *_expert_list(experts, slots), _p(offsets),
-        _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _int_array(_plan3(gate_up_plan) + _plan3(down_plan)), _s(stream)))
+        _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _int_array(_plan3(gate_up_plan) + _plan3(down_plan)), fail_at,
+        _s(stream)))
 
 
 def ft_cache_simulate(num_layers, num_experts, capacity, ops):

@@ -54,6 +54,7 @@ struct Fp8Gemm {
   long long ldo;
   int out_bf16;
   int* err;
+  int fail_at = -1;           // tests: the chunk or tile of a CTA in which a role waits for what never comes
 };
 // mode 0: gate/up + SwiGLU + quantisation, mode 1: the product itself.
 cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& groups, const Fp8Gemm& p, int num_sms,

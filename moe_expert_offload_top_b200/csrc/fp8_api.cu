@@ -88,6 +88,8 @@ Plan plan(int mode, long long rows, int groups, int N, int K, int sms, bool alig
   }
   return best;
 }
+// The chunk or tile of every CTA that a test lets fail; -1: none.
+bool valid_fail(int fail_at) { return fail_at >= -1 && fail_at <= (1 << 20); }
 // A plan that the kernels can run: the token counts of `mode`, K in 1, 2, 4 or 8 parts of a block at least.
 bool valid(int mode, const Plan& p, int K) {
   if (p.nt == 0) return true;
@@ -116,11 +118,11 @@ int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stre
 // ft_gemm_fp8, by `forced` where that is given.
 int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
              const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
-             const Plan* forced, void* stream) {
+             const Plan* forced, int fail_at, void* stream) {
   if (M < 0 || N < 0 || K < 1) return bad(call, "invalid size");
   if (lda < K || ldw < K || ldo < N) return bad(call, "a row stride is smaller than the row");
   if (lda % 16 || ldw % 16) return bad(call, "lda and ldw must be multiples of 16");
-  if (forced && !valid(1, *forced, K)) return bad(call, "no such plan");
+  if (forced && (!valid(1, *forced, K) || !valid_fail(fail_at))) return bad(call, "no such plan");
   if (M == 0 || N == 0) return FT_OK;
   if (!a || !a_scales || !w || !w_scales || !out || !err) return bad(call, "null pointer");
   if (!aligned(a, 16) || !aligned(w, 16)) return bad(call, "a and w must be 16-byte aligned");
@@ -143,7 +145,8 @@ int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scal
   groups.expert[0] = -1;   // all M rows
   groups.z[0] = 0;
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(w_scales);
-  const ftk::Fp8Gemm p{a_scales, {ws, ws}, 0, nullptr, nullptr, M, 0, N, K, out, nullptr, ldo, out_is_bf16 != 0, err};
+  const ftk::Fp8Gemm p{a_scales, {ws, ws}, 0, nullptr, nullptr, M, 0, N, K, out, nullptr, ldo, out_is_bf16 != 0, err,
+                       fail_at};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = pl.nt ? ftk::launch_fp8_stream(1, pl.nt, pl.split, pl.chunks, m, groups, p, false, s)
                               : ftk::launch_fp8_gemm(1, m, groups, p, sms, s);
@@ -154,13 +157,14 @@ int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scal
 int expert_ffn_fp8(const char* call, const void* x, long long ldx, const float* x_scales, int T, int H, int I,
                    int top_k, const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
                    const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
-                   const Plan* forced, void* stream) {
+                   const Plan* forced, int fail_at, void* stream) {
   if (T < 0 || top_k < 1 || top_k > FT_MAX_TOPK || n_list < 0 || n_list > ftk::kMaxList || n_slots < 1)
     return bad(call, "invalid size");
   if (H < 16 || I < 16 || H % 16 || I % 16) return bad(call, "H and I must be multiples of 16");
   if ((long long)T * (top_k + 1) > 0x7FFFFFFF) return bad(call, "T * (top_k + 1) is above 2^31 - 1");
   if (ldx < H || ldx % 16) return bad(call, "ldx must be a multiple of 16 of at least H");
-  if (forced && (!valid(0, forced[0], H) || !valid(1, forced[1], I))) return bad(call, "no such plan");
+  if (forced && (!valid(0, forced[0], H) || !valid(1, forced[1], I) || !valid_fail(fail_at)))
+    return bad(call, "no such plan");
   if (T == 0 || n_list == 0) return FT_OK;
   if (!x || !x_scales || !weights || !experts || !slots || !offsets || !perm || !h || !h_scales || !y || !err)
     return bad(call, "null pointer");
@@ -187,9 +191,10 @@ int expert_ffn_fp8(const char* call, const void* x, long long ldx, const float* 
   const int sms = num_sms();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* ws = w + 3 * n;
-  const ftk::Fp8Gemm g{x_scales, {ws, ws + sb}, (long long)blob, offsets, perm, T, top_k, I, H, h, h_scales, I, 0, err};
+  const ftk::Fp8Gemm g{x_scales, {ws, ws + sb}, (long long)blob, offsets, perm, T, top_k, I, H, h, h_scales, I, 0, err,
+                       fail_at};
   const ftk::Fp8Gemm d{h_scales, {ws + 2 * sb, ws + 2 * sb}, (long long)blob, offsets, perm, T, top_k, H, I,
-                       y, nullptr, H, 0, err};
+                       y, nullptr, H, 0, err, fail_at};
   // The launches of one product of some of the groups, `rows` rows each.  The gate/up tiles find
   // the pairs' token rows in the rows of y that the down product writes last.
   const char* what = "launch: ";
@@ -273,7 +278,7 @@ int ft_gemm_fp8(const void* a, long long lda, const float* a_scales, const void*
                 const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
                 void* stream) {
   return gemm_fp8("ft_gemm_fp8", a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, nullptr,
-                  stream);
+                  -1, stream);
 }
 
 size_t ft_fp8_blob_bytes(int H, int I) {
@@ -287,7 +292,7 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
                       const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
                       void* stream) {
   return expert_ffn_fp8("ft_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, n_list,
-                        offsets, perm, h, h_scales, y, err, nullptr, stream);
+                        offsets, perm, h, h_scales, y, err, nullptr, -1, stream);
 }
 
 int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms, int rows_aligned, int* plan3) {
@@ -302,21 +307,21 @@ int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms,
 
 int ft_debug_gemm_fp8(const void* a, long long lda, const float* a_scales, const void* w, long long ldw,
                       const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
-                      const int* plan3, void* stream) {
+                      const int* plan3, int fail_at, void* stream) {
   if (!plan3) return bad("ft_debug_gemm_fp8", "null pointer");
   const Plan p{plan3[0], plan3[1], plan3[2]};
   return gemm_fp8("ft_debug_gemm_fp8", a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, &p,
-                  stream);
+                  fail_at, stream);
 }
 
 int ft_debug_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
                             const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
                             const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,
-                            const int* plan6, void* stream) {
+                            const int* plan6, int fail_at, void* stream) {
   if (!plan6) return bad("ft_debug_expert_ffn_fp8", "null pointer");
   const Plan p[2] = {{plan6[0], plan6[1], plan6[2]}, {plan6[3], plan6[4], plan6[5]}};
   return expert_ffn_fp8("ft_debug_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots,
-                        n_list, offsets, perm, h, h_scales, y, err, p, stream);
+                        n_list, offsets, perm, h, h_scales, y, err, p, fail_at, stream);
 }
 
 }  // extern "C"

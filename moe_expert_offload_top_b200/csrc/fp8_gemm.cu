@@ -39,7 +39,7 @@
 // both, so silu(gate) * up stays inside a thread.
 //
 // Every wait is bounded: a thread that gives up records 121-125 in *err and raises the CTA's
-// abort flag; all roles then leave and TMEM is released.
+// abort flag; all roles then leave, with their copies and MMAs landed, and TMEM is released.
 #include "fp8.hpp"
 #include "fp8_common.cuh"
 #include "fp8_mma.cuh"
@@ -58,7 +58,7 @@ constexpr int FK = 8;         // blocks of K per chunk of factors
 constexpr int CONTROL_REGS = 56, SUM_REGS = 224;
 
 struct Smem {
-  uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves;
+  uint64_t full[STAGES], done[STAGES], tempty[2], ffull[2], fempty[2], halves, never;
   uint32_t tmem_base;
   int abort;
   int mt_start[kMaxList + 1];   // prefix of M-tiles over the groups
@@ -122,6 +122,7 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
       mbar_init(&S->fempty[b], SUM_WARPS);
     }
     mbar_init(&S->halves, SUM_WARPS);
+    mbar_init(&S->never, 1);
     S->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -173,6 +174,10 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
     if (warp == 0) {   // ------------------------------------------------ TMA producer
       int it = 0;
       for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+        if (t == (int)blockIdx.x + p.fail_at * (int)gridDim.x) {
+          never_wait(&S->never, abort_flag, err, 121);
+          break;
+        }
         int g, m, n;
         decode(t, g, m, n);
         const int row0 = S->row_start[g] + m * BM, z = groups.z[g];
@@ -217,6 +222,8 @@ fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Ge
         }
         __syncwarp();
       }
+      // drain: the last commit stands for every MMA issued (the sums may have given up on them)
+      if (lane == 0 && it > 0) mbar_drain(&S->done[(it - 1) % STAGES], ((it - 1) / STAGES) & 1);
     } else {   // ---------------------------------------------------------- factors
       const int r0 = threadIdx.x - 64;   // rows r0 and r0 + 64 of the tile
       const int NB = (p.N + kFp8Block - 1) / kFp8Block;

@@ -44,6 +44,12 @@ FT_DEVICE bool warp_wait2(uint64_t* b0, uint32_t parity0, uint64_t* b1, uint32_t
   const bool ok = mbar_wait(b0, parity0, abort_flag, err, code) && mbar_wait(b1, parity1, abort_flag, err, code);
   return __all_sync(0xFFFFFFFFu, ok);
 }
+// The wait of a test for the way out: on a barrier that nothing arrives on, for 1 ms.
+FT_DEVICE void never_wait(uint64_t* b, volatile int* abort_flag, int* err, int code) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_wait(b, 0, abort_flag, err, code, 1000000ull);
+  __syncwarp();
+}
 // One arrival for the warp, behind everything its lanes did before.
 FT_DEVICE void warp_arrive(uint64_t* b) {
   __syncwarp();

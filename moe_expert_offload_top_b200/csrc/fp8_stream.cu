@@ -20,8 +20,9 @@
 // of all ranks in rank order (the result does not depend on timing), and stores them.
 // Stores: a warp holds 128 consecutive columns of one output row, and so a whole scale block of h.
 //
-// Every wait is bounded as in fp8_gemm.cu (codes 126-129); the cluster barriers are reached by
-// every thread whatever its role met.
+// Every wait is bounded as in fp8_gemm.cu (codes 126-129).  A CTA that gave up stores nothing
+// more and leaves out the roles of its later chunks, whose barriers are no longer at the phases
+// that `it` and `ch` tell; the cluster barriers are reached by every thread whatever its role met.
 #include "fp8.hpp"
 #include "fp8_common.cuh"
 #include "fp8_mma.cuh"
@@ -36,7 +37,7 @@ constexpr int MAX_STAGES = 8;
 
 template <int COLS>
 struct Ctrl {
-  uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_STAGES], ffull[2], fempty[2];
+  uint64_t full[MAX_STAGES], done[MAX_STAGES], tempty[MAX_STAGES], ffull[2], fempty[2], never;
   uint32_t tmem_base;
   int abort;
   alignas(16) float factor[2][FK][COLS];
@@ -136,6 +137,7 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         mbar_init(&S->ffull[b], 2);
         mbar_init(&S->fempty[b], 4 * C::SW);
       }
+      mbar_init(&S->never, 1);
       S->abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -160,9 +162,12 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
   else asm volatile("griddepcontrol.wait;" ::: "memory");
 
   int it = 0, ch = 0;   // blocks of K and chunks of factors so far
-  for (int t0 = blockIdx.z * NT; t0 < rows; t0 += gridDim.z * NT) {
+  bool gone = false;    // the CTA gave up in an earlier chunk: the same for all its threads
+  for (int t0 = blockIdx.z * NT, chunk = 0; t0 < rows; t0 += gridDim.z * NT, ++chunk) {
     const int valid = min(NT, rows - t0), row0 = first + t0;
-    if (warp == 0) {   // -------------------------------------------------- TMA producer
+    if (gone) {
+      // only the barriers
+    } else if (warp == 0) {   // -------------------------------------------------- TMA producer
       int tok[4];
       if (MODE == 0) {   // lane l < NT / 4 gathers tokens 4 l .. 4 l + 3; tokens past the last repeat it
 #pragma unroll
@@ -209,6 +214,10 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         }
         __syncwarp();
       }
+      // drain: the last commit stands for every MMA issued (the sums may have given up on them)
+      if (lane == 0 && i > it) mbar_drain(&S->done[(i - 1) % STAGES], ((i - 1) / STAGES) & 1);
+    } else if (warp < 4 && chunk == p.fail_at) {
+      never_wait(&S->never, abort_flag, err, 129);
     } else if (warp < 4) {   // --------------------------------------------- factors
       const int t = threadIdx.x - 64;
       constexpr int OWN = (NT + 63) / 64;   // tokens of this thread: t, t + 64
@@ -255,9 +264,9 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
       for (int i = 0; i < CHUNKS * 16; ++i) acc[i] = 0.f;
       auto column = [&](int j) { return (j / (C1 / 16)) * NT + half * C1 + (j % (C1 / 16)) * 16; };
       int i = it, c = ch;
+      bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int s = i % STAGES, b = i % BUFS, f = (kb - kb0) % FK, fb = c & 1;
-        bool ok = true;
         if (f == 0) ok = warp_wait(&S->ffull[fb], (c >> 1) & 1, abort_flag, err, 128);
         ok = ok && warp_wait(&S->done[s], (i / STAGES) & 1, abort_flag, err, 128);
         if (!ok) break;
@@ -282,10 +291,12 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
         c += f == FK - 1 || kb == kb1 - 1;
       }
       // Every block of this CTA has been multiplied: the ring's memory is free for the sums.
+      if (ok) {
 #pragma unroll
-      for (int j = 0; j < CHUNKS; ++j)
+        for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) part[(column(j) + x) * 128 + q * 32 + lane] = acc[16 * j + x];
+          for (int x = 0; x < 16; ++x) part[(column(j) + x) * 128 + q * 32 + lane] = acc[16 * j + x];
+      }
     }
     __syncwarp();
     it += kb1 - kb0;
@@ -293,7 +304,8 @@ fp8_stream_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ 
     if (split > 1) cluster_sync(); else __syncthreads();
 
     // Columns of this rank, added over the ranks: a warp takes a token, a lane four weight rows.
-    if (warp >= 4) {
+    gone = *abort_flag;   // no role is at work between the barriers
+    if (warp >= 4 && !gone) {
       const int c1 = min(NT * (rank + 1) / split, valid);
       const int col = n * 128 + 4 * lane;
 #pragma unroll (MODE == 1 ? 2 : 1)

@@ -51,3 +51,9 @@ def test_forced_calls_check_their_arguments(change, word):
 def test_forced_empty_calls_do_nothing():
     ft.ft_debug_gemm_fp8(*dict(GEMM, M=0, plan=(0, 1, 1)).values())
     ft.ft_debug_expert_ffn_fp8(*dict(FFN, T=0, gate_up=(0, 1, 1), down=(0, 1, 1)).values())
+
+
+@pytest.mark.parametrize("fail_at", [-2, (1 << 20) + 1])
+def test_failing_chunk_is_checked(fail_at):
+    _refused(ft.ft_debug_gemm_fp8, dict(GEMM, plan=(0, 1, 1), fail_at=fail_at), {}, "plan")
+    _refused(ft.ft_debug_expert_ffn_fp8, dict(FFN, gate_up=(0, 1, 1), down=(0, 1, 1), fail_at=fail_at), {}, "plan")

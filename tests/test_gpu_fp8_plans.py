@@ -96,7 +96,7 @@ def test_gemm_by_plan_streams_repeats_and_graph(plan):
     first, err = torch.zeros((M, N), device=DEV), _err()
 
     def call(out, stream=None):
-        ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, plan, stream)
+        ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, plan, -1, stream)
     call(first)
     torch.cuda.synchronize()
     outs = [torch.zeros((M, N), device=DEV) for _ in range(8)]
@@ -125,7 +125,7 @@ class PlannedFfn(Ffn):
     def run(self, stream=None, experts=None, slots=None):
         ft.ft_debug_expert_ffn_fp8(self.x, self.ldx, self.xs, self.T, self.H, self.I, self.k, self.weights, self.n_slots,
                                    self.experts if experts is None else experts, self.slots if slots is None else slots,
-                                   self.offsets, self.perm, self.h, self.hs, self.y, self.err, *self.plans, stream)
+                                   self.offsets, self.perm, self.h, self.hs, self.y, self.err, *self.plans, -1, stream)
 
 
 # every gate/up form, each with another form of the down product
@@ -254,3 +254,56 @@ def test_quantised_rows_are_the_formula_bit_for_bit(T, H, bf16):
     ft.ft_quantize_fp8(x.to(DEV), H, bf16, T, H, q, H, s)
     assert np.array_equal(s.cpu().numpy(), scale)
     assert np.array_equal(fp8.decode(_bytes(q)), fp8.round_e4m3(v))
+
+
+# ------------------------------------- a device wait that runs out (1 ms) --
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+@pytest.mark.parametrize("nt,split", [(16, 1), (16, 8), (32, 4), (128, 2)])
+def test_stream_product_gives_up(nt, split, at):
+    """A wait of every CTA's chunk `at` gives up: the chunks before it are right, it and those behind it
+    are left unwritten, the call returns, and the next call is right."""
+    M, N, K = 5 * nt - 3, 300, 2048
+    ld, a, w, sa, sw = _gemm_case(M, N, K, nt)
+    want, err = torch.zeros((M, N), device=DEV), _err()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, want, N, err, (nt, split, 1))
+    assert err.item() == 0
+    out = torch.full((M, N), 77.0, device=DEV)
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, (nt, split, 1), at)
+    assert err.item() == 129
+    assert torch.equal(out[:nt * at], want[:nt * at]) and (out[nt * at:] == 77).all()
+    err.zero_()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, (nt, split, 1))
+    assert err.item() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("at", [0, 1])
+def test_tile_product_gives_up(at):
+    """The same for the tiles: a CTA's first tiles are right, the one that gave up and later ones unwritten."""
+    ctas, M, N, K = _sms(), 2560, 4096, 1280      # 320 tiles of 128 x 256, column by column of tiles
+    ld, a, w, sa, sw = _gemm_case(M, N, K, 6)
+    want, err = torch.zeros((M, N), device=DEV), _err()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, want, N, err, TILES)
+    assert err.item() == 0
+    out = torch.full((M, N), 77.0, device=DEV)
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, TILES, at)
+    assert err.item() == 121
+    for t in range(M // 128 * (N // 256)):
+        r, c = slice(t % 20 * 128, t % 20 * 128 + 128), slice(t // 20 * 256, t // 20 * 256 + 256)
+        assert torch.equal(out[r, c], want[r, c]) if t < ctas * at else (out[r, c] == 77).all()
+    err.zero_()
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, False, out, N, err, TILES)
+    assert err.item() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("gate_up,down", [((16, 2, 1), (16, 1, 1)), ((64, 1, 1), (128, 1, 1)), (TILES, TILES)])
+def test_expert_ffn_gives_up(gate_up, down):
+    f = PlannedFfn(150, 400, 272, 3, 2, True, seed=8)
+    ft.ft_debug_expert_ffn_fp8(f.x, f.ldx, f.xs, f.T, f.H, f.I, f.k, f.weights, f.n_slots, f.experts, f.slots, f.offsets,
+                               f.perm, f.h, f.hs, f.y, f.err, gate_up, down, 0)
+    assert f.err.item() == (129 if gate_up[0] else 121)
+    assert (f.h == 0x55).all() and (f.hs == -1).all()
+    f.buffers()
+    f.plans = gate_up, down
+    f.run()
+    f.check()
