@@ -584,7 +584,7 @@ FT_API int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, i
  *   a: [M][K] e4m3, rows lda bytes apart; a_scales: [M][ceil(K / 128)] f32 (as ft_rmsnorm_fp8 and
  *   ft_quantize_fp8 write them).  w: [N][K] e4m3, rows ldw bytes apart; w_scales:
  *   [ceil(N / 128)][ceil(K / 128)] f32.  out: [M][N], rows ldo elements apart, bf16 (round to
- *   nearest even) if out_is_bf16 else f32.  Any M, N and K >= 1; lda and ldw multiples of 16,
+ *   nearest even) if out_is_bf16 else f32.  1 <= M, N, K <= 2^31 - 2^16; lda and ldw multiples of 16,
  *   a and w 16-byte aligned; bytes past K of a row are not read as values.
  *   err: a DEVICE int, 0 before the call; a kernel whose bounded pipeline wait gives up writes
  *   121-129 there (the outputs are then incomplete). */

@@ -15,6 +15,9 @@ namespace ftk {
 
 constexpr int kFp8Block = 128;
 constexpr int kFp8MaxWidth = 32768;   // widest row of the norm and the quantisation
+// Largest row, column or pair count of a product: the kernels round such numbers up to tiles, and step
+// past the last by less than 2^16, in 32 bits.
+constexpr int kFp8MaxCount = 0x7FFFFFFF - 0xFFFF;
 inline int fp8_blocks(long long n) { return (int)((n + kFp8Block - 1) / kFp8Block); }
 
 // Rows of x (plus residual) -> norm -> e4m3 rows.  Strides in elements.

@@ -120,6 +120,8 @@ int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scal
              const float* w_scales, int M, int N, int K, int out_is_bf16, void* out, long long ldo, int* err,
              const Plan* forced, int fail_at, void* stream) {
   if (M < 0 || N < 0 || K < 1) return bad(call, "invalid size");
+  if (M > ftk::kFp8MaxCount || N > ftk::kFp8MaxCount || K > ftk::kFp8MaxCount)
+    return bad(call, "M, N or K is above 2^31 - 2^16");
   if (lda < K || ldw < K || ldo < N) return bad(call, "a row stride is smaller than the row");
   if (lda % 16 || ldw % 16) return bad(call, "lda and ldw must be multiples of 16");
   if (forced && (!valid(1, *forced, K) || !valid_fail(fail_at))) return bad(call, "no such plan");
@@ -296,7 +298,8 @@ int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T
 }
 
 int ft_debug_fp8_plan(int mode, int rows, int groups, int N, int K, int num_sms, int rows_aligned, int* plan3) {
-  if ((mode != 0 && mode != 1) || rows < 0 || groups < 1 || N < 1 || K < 1 || num_sms < 1 || !plan3)
+  if ((mode != 0 && mode != 1) || rows < 0 || groups < 1 || N < 1 || K < 1 || num_sms < 1 || !plan3 ||
+      rows > ftk::kFp8MaxCount || N > ftk::kFp8MaxCount || K > ftk::kFp8MaxCount)
     return bad("ft_debug_fp8_plan", "invalid argument");
   const Plan p = plan(mode, rows, groups, N, K, num_sms, rows_aligned != 0);
   plan3[0] = p.nt;

@@ -27,7 +27,7 @@ def test_every_plan_is_one_that_the_kernels_take(mode):
 
 
 @pytest.mark.parametrize("args", [(2, 1, 1, 1, 1), (0, -1, 1, 1, 1), (0, 1, 0, 1, 1), (0, 1, 1, 0, 1), (0, 1, 1, 1, 0),
-                                  (0, 1, 1, 1, 1, 0)])
+                                  (0, 1, 1, 1, 1, 0), (1, 1, 1, 2 ** 31 - 1, 1)])
 def test_plan_refusals(args):
     with pytest.raises(ft.FtError) as e:
         ft.ft_debug_fp8_plan(*args)
@@ -57,3 +57,17 @@ def test_forced_empty_calls_do_nothing():
 def test_failing_chunk_is_checked(fail_at):
     _refused(ft.ft_debug_gemm_fp8, dict(GEMM, plan=(0, 1, 1), fail_at=fail_at), {}, "plan")
     _refused(ft.ft_debug_expert_ffn_fp8, dict(FFN, gate_up=(0, 1, 1), down=(0, 1, 1), fail_at=fail_at), {}, "plan")
+
+
+TOP = 2 ** 31 - 2 ** 16
+
+
+@pytest.mark.parametrize("change", [dict(M=TOP + 1), dict(M=2 ** 31 - 1), dict(N=TOP + 1, ldo=2 ** 31),
+                                    dict(N=2 ** 31 - 1, ldo=2 ** 31), dict(K=TOP + 1, lda=2 ** 31, ldw=2 ** 31),
+                                    dict(K=2 ** 31 - 1, lda=2 ** 31, ldw=2 ** 31)])
+def test_products_whose_tiles_would_pass_32_bits_are_refused(change):
+    _refused(ft.ft_gemm_fp8, GEMM, change, "2^31 - 2^16")
+
+
+def test_the_largest_product_sizes_are_not_refused_for_their_size():
+    _refused(ft.ft_gemm_fp8, GEMM, dict(M=TOP, N=TOP, ldo=TOP, K=TOP, lda=2 ** 31, ldw=2 ** 31, a=None), "null")
