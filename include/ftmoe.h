@@ -611,7 +611,7 @@ FT_API size_t ft_fp8_blob_bytes(int H, int I);
  *   quantised rows between the two products.  y: [T*top_k + T][H] f32, written (before that an
  *   owned row may hold its token's codes).  Rows that no entry owns are left as they are.
  *   The buffers must not overlap.  Every listed expert must be below the E of offsets.
- *   H and I: multiples of 16.  T * (top_k + 1) < 2^31.  err: as in ft_gemm_fp8. */
+ *   H and I: multiples of 16.  H, I and T * (top_k + 1): at most 2^31 - 2^16.  err: as in ft_gemm_fp8. */
 FT_API int ft_expert_ffn_fp8(const void* x, long long ldx, const float* x_scales, int T, int H, int I, int top_k,
                              const void* weights, int n_slots, const int* experts, const int* slots, int n_list,
                              const int* offsets, const int* perm, void* h, float* h_scales, float* y, int* err,

@@ -163,7 +163,8 @@ int expert_ffn_fp8(const char* call, const void* x, long long ldx, const float* 
   if (T < 0 || top_k < 1 || top_k > FT_MAX_TOPK || n_list < 0 || n_list > ftk::kMaxList || n_slots < 1)
     return bad(call, "invalid size");
   if (H < 16 || I < 16 || H % 16 || I % 16) return bad(call, "H and I must be multiples of 16");
-  if ((long long)T * (top_k + 1) > 0x7FFFFFFF) return bad(call, "T * (top_k + 1) is above 2^31 - 1");
+  if (H > ftk::kFp8MaxCount || I > ftk::kFp8MaxCount) return bad(call, "H or I is above 2^31 - 2^16");
+  if ((long long)T * (top_k + 1) > ftk::kFp8MaxCount) return bad(call, "T * (top_k + 1) is above 2^31 - 2^16");
   if (ldx < H || ldx % 16) return bad(call, "ldx must be a multiple of 16 of at least H");
   if (forced && (!valid(0, forced[0], H) || !valid(1, forced[1], I) || !valid_fail(fail_at)))
     return bad(call, "no such plan");

@@ -71,3 +71,15 @@ def test_products_whose_tiles_would_pass_32_bits_are_refused(change):
 
 def test_the_largest_product_sizes_are_not_refused_for_their_size():
     _refused(ft.ft_gemm_fp8, GEMM, dict(M=TOP, N=TOP, ldo=TOP, K=TOP, lda=2 ** 31, ldw=2 ** 31, a=None), "null")
+
+
+@pytest.mark.parametrize("change", [
+    dict(T=(2 ** 31 - 1) // 3), dict(T=(2 ** 31 - 2 ** 14) // 3), dict(T=TOP // 3 + 1), dict(T=TOP // 17 + 1, top_k=16),
+    dict(H=2 ** 31 - 16, ldx=2 ** 31), dict(I=2 ** 31 - 16)])
+def test_expert_lists_whose_rows_would_pass_32_bits_are_refused(change):
+    """The copy of the pairs' rows steps past the last row by up to 8192: 32 bits have to hold that."""
+    _refused(ft.ft_expert_ffn_fp8, FFN, change, "2^31 - 2^16")
+
+
+def test_the_most_pairs_are_not_refused_for_their_number():
+    _refused(ft.ft_expert_ffn_fp8, FFN, dict(T=TOP // 3, h=None), "null")
