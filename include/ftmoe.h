@@ -562,7 +562,7 @@ FT_API int ft_expert_ffn_decode_noalloc(const void* x, int T, int H, int I, int 
  * scale NaN or infinite (so every value of the block is NaN) and leaves the other rows alone.
  *   x: [T][H], rows ldx elements apart, bf16 if x_is_bf16 else f32; residual (may be NULL) and
  *   residual_out (may be NULL; receives r): [T][H], rows ldr apart, x's type; residual_out may
- *   be residual, or x when ldx == ldr; otherwise the buffers must not overlap.  weight: [H], x's
+ *   be residual, or x when ldx == ldr (refused when not, for T > 1); otherwise the buffers must not overlap.  weight: [H], x's
  *   type.  y (may be NULL): [T][H] contiguous, x's type.
  *   q (may be NULL, y not both): bytes, rows ldq apart; the bytes past H of a row are not
  *   written.  scales: [T][ceil(H / 128)] f32.  1 <= H <= 32768, any strides of at least H.

@@ -104,6 +104,8 @@ int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stre
   if (p.H > ftk::kFp8MaxWidth) return bad(call, "H is above 32768");
   if (p.ldx < p.H || (p.q && p.ldq < p.H) || ((p.residual || p.residual_out) && p.ldr < p.H))
     return bad(call, "a row stride is smaller than H");
+  if (p.T > 1 && p.residual_out && p.residual_out == p.x && p.ldx != p.ldr)   // rows written before they are read
+    return bad(call, "residual_out may be x only where ldx and ldr are the same stride");
   if (p.T == 0) return FT_OK;
   if (!p.x || (!p.q && !p.y) || (p.q && !p.scales)) return bad(call, "null pointer");
   if (!aligned(p.x, es) || !aligned(p.residual, es) || !aligned(p.weight, es) || !aligned(p.residual_out, es) ||

@@ -2,7 +2,7 @@
 import pytest
 
 import moe_expert_offload_top_b200 as ft
-from test_fp8_cpu import FFN, GEMM, _refused
+from test_fp8_cpu import FFN, GEMM, NORM, P, _refused
 
 
 @pytest.mark.parametrize("mode,rows,groups,N,K,want", [
@@ -83,3 +83,11 @@ def test_expert_lists_whose_rows_would_pass_32_bits_are_refused(change):
 
 def test_the_most_pairs_are_not_refused_for_their_number():
     _refused(ft.ft_expert_ffn_fp8, FFN, dict(T=TOP // 3, h=None), "null")
+
+
+def test_norm_over_x_in_rows_of_another_stride_is_refused():
+    base = dict(NORM, residual=P + (1 << 16))     # residual_out is x
+    _refused(ft.ft_rmsnorm_fp8, base, dict(ldx=512), "stride")
+    _refused(ft.ft_rmsnorm_fp8, base, dict(ldr=272, residual=None), "stride")
+    _refused(ft.ft_rmsnorm_fp8, base, dict(ldx=512, T=1, scales=None), "null")     # one row: any strides
+    _refused(ft.ft_rmsnorm_fp8, base, dict(scales=None), "null")
