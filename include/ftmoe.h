@@ -550,7 +550,8 @@ FT_API int ft_expert_ffn_decode_noalloc(const void* x, int T, int H, int I, int 
  * All four allocate nothing, launch on `stream`, return after the launch and keep nothing
  * between calls, so they may be captured into a graph and run on several streams at once
  * (each on its own outputs and scratch).  All pointers but the host lists are device memory of the
- * current device; the output is checked (FT_ERR_INVALID).  Every refusal leaves a message
+ * current device; the output is checked (FT_ERR_INVALID), and the Python binding refuses a host tensor,
+ * or tensors of two devices, among the others.  Every refusal leaves a message
  * in ft_last_error(NULL).  Sizes of 0 tokens, rows or columns are calls that do nothing.
  * ------------------------------------------------------------------------ */
 

@@ -151,6 +151,21 @@ def _p(a):
     raise TypeError("cannot take the address of %r" % type(a))
 
 
+def _dp(call, *tensors):
+    """Pointers of device tensors (ints and None pass).  A host tensor, or one of another device than the
+    rest, would fault the kernel: refused.  That the rest is the current device's, the C call
+    checks of its output."""
+    dev, out = None, []
+    for a in tensors:
+        if a is not None and not isinstance(a, int):
+            d = a.get_device() if hasattr(a, "get_device") else -1
+            if d < 0 or (dev is not None and d != dev):
+                raise FtError(FT_ERR_INVALID, call + ": a tensor is not memory of the current device")
+            dev, a = d, a.data_ptr()
+        out.append(a)
+    return out
+
+
 def _s(stream):
     if stream is None:
         return None
@@ -356,40 +371,47 @@ def ft_combine(y, gates, inv, T, H, top_k, has_shared, out_is_bf16, out, stream=
 
 
 def ft_rmsnorm_fp8(x, ldx, residual, ldr, weight, x_is_bf16, T, H, eps, residual_out, y, q, ldq, scales, stream=None):
-    return _check(None, _lib.ft_rmsnorm_fp8(_p(x), ldx, _p(residual), ldr, _p(weight), int(x_is_bf16), T, H, eps,
-                                            _p(residual_out), _p(y), _p(q), ldq, _p(scales), _s(stream)))
+    x, residual, weight, residual_out, y, q, scales = _dp("ft_rmsnorm_fp8", x, residual, weight, residual_out, y, q,
+                                                          scales)
+    return _check(None, _lib.ft_rmsnorm_fp8(x, ldx, residual, ldr, weight, int(x_is_bf16), T, H, eps, residual_out, y, q,
+                                            ldq, scales, _s(stream)))
 
 
 def ft_quantize_fp8(x, ldx, x_is_bf16, T, H, q, ldq, scales, stream=None):
-    return _check(None, _lib.ft_quantize_fp8(_p(x), ldx, int(x_is_bf16), T, H, _p(q), ldq, _p(scales), _s(stream)))
+    x, q, scales = _dp("ft_quantize_fp8", x, q, scales)
+    return _check(None, _lib.ft_quantize_fp8(x, ldx, int(x_is_bf16), T, H, q, ldq, scales, _s(stream)))
 
 
 def ft_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, stream=None):
-    return _check(None, _lib.ft_gemm_fp8(_p(a), lda, _p(a_scales), _p(w), ldw, _p(w_scales), M, N, K, int(out_is_bf16),
-                                         _p(out), ldo, _p(err), _s(stream)))
+    a, a_scales, w, w_scales, out, err = _dp("ft_gemm_fp8", a, a_scales, w, w_scales, out, err)
+    return _check(None, _lib.ft_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, int(out_is_bf16), out, ldo, err,
+                                         _s(stream)))
 
 
 def ft_fp8_blob_bytes(H, I):
     return _lib.ft_fp8_blob_bytes(H, I)
 
 
-def _expert_list(experts, slots):
-    """(experts, slots, n_list) as the C calls take host lists."""
+def _ffn_fp8_args(call, x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets, perm, h, h_scales,
+                  y, err):
+    """The arguments of the fp8 FFN as the C calls take them."""
     if len(experts) != len(slots):
         raise ValueError("experts and slots must have the same length")
-    return _int_array(list(experts) or [0]), _int_array(list(slots) or [0]), len(experts)
-
-
-def _plan3(plan):
-    nt, split, chunks = plan
-    return nt, split, chunks
+    x, x_scales, weights, *rest = _dp(call, x, x_scales, weights, offsets, perm, h, h_scales, y, err)
+    ex, sl = _int_array(list(experts) or [0]), _int_array(list(slots) or [0])
+    return (x, ldx, x_scales, T, H, I, top_k, weights, n_slots, ex, sl, len(experts), *rest)
 
 
 def ft_expert_ffn_fp8(x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets, perm, h, h_scales, y,
                       err, stream=None):
     return _check(None, _lib.ft_expert_ffn_fp8(
-        _p(x), ldx, _p(x_scales), T, H, I, top_k, _p(weights), n_slots, *_expert_list(experts, slots), _p(offsets),
-        _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _s(stream)))
+        *_ffn_fp8_args("ft_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets,
+                       perm, h, h_scales, y, err), _s(stream)))
+
+
+def _plan3(plan):
+    nt, split, chunks = plan
+    return nt, split, chunks
 
 
 def ft_debug_fp8_plan(mode, rows, groups, N, K, num_sms=148, rows_aligned=True):
@@ -401,17 +423,17 @@ def ft_debug_fp8_plan(mode, rows, groups, N, K, num_sms=148, rows_aligned=True):
 
 def ft_debug_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, out_is_bf16, out, ldo, err, plan, fail_at=-1,
                       stream=None):
-    return _check(None, _lib.ft_debug_gemm_fp8(_p(a), lda, _p(a_scales), _p(w), ldw, _p(w_scales), M, N, K,
-                                               int(out_is_bf16), _p(out), ldo, _p(err), _int_array(_plan3(plan)), fail_at,
-                                               _s(stream)))
+    a, a_scales, w, w_scales, out, err = _dp("ft_debug_gemm_fp8", a, a_scales, w, w_scales, out, err)
+    return _check(None, _lib.ft_debug_gemm_fp8(a, lda, a_scales, w, ldw, w_scales, M, N, K, int(out_is_bf16), out, ldo,
+                                               err, _int_array(_plan3(plan)), fail_at, _s(stream)))
 
 
 def ft_debug_expert_ffn_fp8(x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots, offsets, perm, h,
                             h_scales, y, err, gate_up_plan, down_plan, fail_at=-1, stream=None):
     return _check(None, _lib.ft_debug_expert_ffn_fp8(
-        _p(x), ldx, _p(x_scales), T, H, I, top_k, _p(weights), n_slots, *_expert_list(experts, slots), _p(offsets),
-        _p(perm), _p(h), _p(h_scales), _p(y), _p(err), _int_array(_plan3(gate_up_plan) + _plan3(down_plan)), fail_at,
-        _s(stream)))
+        *_ffn_fp8_args("ft_debug_expert_ffn_fp8", x, ldx, x_scales, T, H, I, top_k, weights, n_slots, experts, slots,
+                       offsets, perm, h, h_scales, y, err),
+        _int_array(_plan3(gate_up_plan) + _plan3(down_plan)), fail_at, _s(stream)))
 
 
 def ft_cache_simulate(num_layers, num_experts, capacity, ops):

@@ -1,8 +1,9 @@
 """How the fp8 products choose their form, and the refusals of forced plans (no GPU)."""
 import pytest
+import torch
 
 import moe_expert_offload_top_b200 as ft
-from test_fp8_cpu import FFN, GEMM, NORM, P, _refused
+from test_fp8_cpu import FFN, GEMM, NORM, P, QUANT, _refused
 
 
 @pytest.mark.parametrize("mode,rows,groups,N,K,want", [
@@ -91,3 +92,35 @@ def test_norm_over_x_in_rows_of_another_stride_is_refused():
     _refused(ft.ft_rmsnorm_fp8, base, dict(ldr=272, residual=None), "stride")
     _refused(ft.ft_rmsnorm_fp8, base, dict(ldx=512, T=1, scales=None), "null")     # one row: any strides
     _refused(ft.ft_rmsnorm_fp8, base, dict(scales=None), "null")
+
+
+CALLS = [(ft.ft_rmsnorm_fp8, NORM, {}), (ft.ft_quantize_fp8, QUANT, {}), (ft.ft_gemm_fp8, GEMM, {}),
+         (ft.ft_expert_ffn_fp8, FFN, {}), (ft.ft_debug_gemm_fp8, GEMM, dict(plan=(0, 1, 1))),
+         (ft.ft_debug_expert_ffn_fp8, FFN, dict(gate_up=(0, 1, 1), down=(0, 1, 1)))]
+
+
+@pytest.mark.parametrize("fn,base,more,name", [(f, b, m, k) for f, b, m in CALLS for k, v in b.items() if v is P])
+def test_host_memory_is_refused(fn, base, more, name):
+    """A kernel that read it would fault the GPU."""
+    host = torch.zeros(1 << 12, dtype=torch.uint8)
+    for value in (host, host.numpy()):
+        _refused(fn, dict(base, **more), {name: value}, "current device")
+
+
+class Elsewhere:
+    """A tensor of some device, as the binding sees one."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return P
+
+
+def test_tensors_of_two_devices_are_refused():
+    for name in ("a", "w_scales", "err"):
+        tensors = {k: Elsewhere(1 if k == name else 0) for k, v in GEMM.items() if v is P}
+        _refused(ft.ft_gemm_fp8, GEMM, tensors, "current device")
