@@ -157,12 +157,18 @@ def _dp(call, *tensors):
     checks of its output."""
     dev, out = None, []
     for a in tensors:
-        if a is not None and not isinstance(a, int):
-            d = a.get_device() if hasattr(a, "get_device") else -1
-            if d < 0 or (dev is not None and d != dev):
+        if a is None or isinstance(a, int):
+            out.append(a)
+            continue
+        try:
+            d = a.get_device()
+        except AttributeError:      # an array: host memory
+            d = -1
+        if d != dev:
+            if d < 0 or dev is not None:
                 raise FtError(FT_ERR_INVALID, call + ": a tensor is not memory of the current device")
-            dev, a = d, a.data_ptr()
-        out.append(a)
+            dev = d
+        out.append(a.data_ptr())
     return out
 
 
