@@ -601,7 +601,9 @@ FT_API size_t ft_fp8_blob_bytes(int H, int I);
 /* SwiGLU FFN of a list of experts on e4m3 weights and rows, from one token to long prefills:
  *     h[q] = silu(W_gate x_t) * (W_up x_t), quantised like every activation row
  *     y[q] = W_down h[q]                                                  (f32)
- * for the pairs q of every entry, as in ft_expert_ffn_prefill: routed expert experts[i] owns q in
+ * silu(a) is within (9 + 2.4 |a|) 2^-24 of its value, but may be 0 below a = -87.3 (|silu(a)| < 1.1e-36);
+ * an infinite or NaN h makes its block's scale infinite or NaN and leaves the other rows alone.
+ * For the pairs q of every entry, as in ft_expert_ffn_prefill: routed expert experts[i] owns q in
  * [offsets[e], offsets[e+1]) with token t = perm[q] / top_k, experts[i] = -1 (the shared expert)
  * q = T*top_k + t for every token t.  An expert is listed at most once.
  *   x: [T][H] e4m3, rows ldx bytes apart (a multiple of 16, 16-byte aligned); x_scales:

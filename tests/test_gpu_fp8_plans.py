@@ -12,7 +12,7 @@ import torch
 
 import moe_expert_offload_top_b200 as ft
 from oracle import fp8
-from test_gpu_fp8 import DEV, UBF, Ffn, _bytes, _dt, _err, _np, _operand, _scales
+from test_gpu_fp8 import DEV, EPS, UBF, Ffn, _bytes, _dt, _err, _norm_bound, _np, _operand, _scales, check_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -218,7 +218,6 @@ def test_expert_ffn_at_sizes_of_the_tiles(T, H, I, E, k, nt):
 @pytest.mark.parametrize("T,H", [(297, 4112), (300, 7168), (400, 9008), (299, 16384)])
 def test_rmsnorm_many_wide_aligned_rows(T, H, bf16):
     """Two chunks per thread: more than 296 aligned rows wider than 4096."""
-    from test_gpu_fp8 import EPS, _norm_bound, check_codes
     g = torch.Generator().manual_seed(H)
     x, res = ((torch.randn((T, H + 16), generator=g) * s).to(_dt(bf16)).to(DEV) for s in (2, 5))
     w = (1 + 0.3 * torch.randn(H, generator=g)).to(_dt(bf16)).to(DEV)
@@ -307,3 +306,86 @@ def test_expert_ffn_gives_up(gate_up, down):
     f.plans = gate_up, down
     f.run()
     f.check()
+
+
+# ------------------------------------------------- SiLU, NaN and infinities --
+
+FORMS = [TILES, (16, 1, 1), (32, 1, 2), (64, 1, 1)]
+
+
+def _planned(T, H, I, E, k, shared, seed, form):
+    f = PlannedFfn(T, H, I, E, k, shared, seed=seed)
+    f.plans = form, (128 if form[0] == 64 else form[0], *form[1:])
+    return f
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_silu_over_its_whole_range(form):
+    """One column of x is 1, so that a = x_scale * gate code and u = x_scale * up code * its scale: from 1e-30 to
+    1e18, where exp(-a) is inf, around the smallest quotients, and far positive.  a is rounded
+    twice (the scales' product, the product with the code), u twice, silu by (9 + 2.4 |a|), the
+    product once, in units of 2^-24; a's error reaches silu times 1 + |a|.  Below -87.3 silu may be 0."""
+    H, I = 144, 144
+    scales = np.float32([1e-30, 1e-3, 0.3, 1.0, 3.7, 9.1, 20.0, 43.0, 58.3, 64.0, 80.0, 86.9, 87.4, 88.0, 88.5, 88.8, 100.0,
+                         1e4, 1e12, 1e18])
+    T = len(scales)
+    f = _planned(T, H, I, 1, 1, False, 3, form)
+    rng = np.random.default_rng(5)
+    x = np.zeros((T, H))
+    x[:, 7] = 1.0
+    gate, up = np.zeros((I, H)), np.zeros((I, H))
+    gate[:, 7] = np.resize([1.0, -1.0, 0.5, -0.5, -0.9375, 0.0625, -2.0 ** -9, -1.125], I)
+    gate[128:, 7] = -1.0     # a block whose scale is that of its negative a
+    up[:, 7] = fp8.round_e4m3(rng.standard_normal(I))
+    raw = np.frombuffer(b"".join(fp8.encode(m).tobytes() for m in (gate, up, np.zeros((H, I)))), dtype=np.uint8)
+    sg, su = np.float32([[1.0, 1.0], [1.0, 1.0]]), np.float32([[0.3, 1.0], [7.0, 1.0]])
+    raw = np.concatenate([raw, np.frombuffer(sg.tobytes() + su.tobytes() + sg.tobytes(), dtype=np.uint8)])
+    f.weights[f.slots[0], :len(raw)] = torch.from_numpy(raw).to(DEV)
+    f.x[:, :H] = torch.from_numpy(fp8.encode(x)).to(DEV)
+    f.xs[:] = torch.from_numpy(scales[:, None]).to(DEV)
+    f.run()
+    assert f.err.item() == 0
+    a = scales[:, None].astype(np.float64) * gate[None, :, 7]
+    u = scales[:, None].astype(np.float64) * np.repeat(su[:, 0].astype(np.float64), 128)[:I] * up[None, :, 7]
+    ref = fp8.silu(a) * u
+    U = 2.0 ** -24
+    bound = np.abs(ref) * U * (2 * (1 + np.abs(a)) + 2 + 9 + 2.4 * np.abs(a) + 1) + np.where(a < -87.3, 1.1e-36 * np.abs(u), 0)
+    h, hs = _bytes(f.h), _np(f.hs)
+    for t in range(T):      # a row by itself: the bounds differ by 60 orders of magnitude
+        worst = np.array([[bound[t, :128].max(), bound[t, 128:].max()]])
+        for b, c in ((0, slice(0, 128)), (1, slice(128, I))):
+            check_codes(h[t:t + 1, c], hs[t:t + 1, b:b + 1], ref[t:t + 1, c], 0.0, worst[:, b:b + 1])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_ffn_keeps_nan_and_infinities_to_their_rows(form):
+    T, H, I, E, k = 70, 272, 272, 4, 2
+    f = _planned(T, H, I, E, k, True, 17, form)
+    f.run()
+    torch.cuda.synchronize()
+    h0, hs0, y0 = f.h.clone(), f.hs.clone(), f.y.clone()
+    f.buffers()
+    f.x[3, 200] = 0x7F                       # a NaN code
+    f.xs[40, 1] = float("nan")               # a NaN scale
+    f.xs[41, 0] = 3e38                       # sums that overflow
+    off, perm = _bytes(f.offsets), _bytes(f.perm)
+    lo, hi = off[2], off[3]
+    n = 3 * H * I                            # expert 2: a NaN in S_up's block of h columns 128 .. 255
+    blob = f.weights[f.slots[2]]
+    sc = blob[n:n + 4 * 3 * 9].view(torch.float32).view(3, 3, 3)
+    sc[1, 1, 0] = float("nan")
+    f.run()
+    torch.cuda.synchronize()
+    assert f.err.item() == 0
+    token = np.concatenate([perm // k, np.arange(T)])
+    bad_rows = torch.from_numpy(np.isin(token, (3, 40, 41))).to(DEV)
+    bad_expert = torch.zeros_like(bad_rows)
+    bad_expert[lo:hi] = True
+    clean = ~bad_rows & ~bad_expert
+    assert torch.equal(f.h[clean], h0[clean]) and torch.equal(f.hs[clean], hs0[clean]) and torch.equal(f.y[clean], y0[clean])
+    nan_rows = torch.from_numpy(np.isin(token, (3, 40))).to(DEV)
+    assert torch.isnan(f.hs[nan_rows]).all() and torch.isnan(f.y[nan_rows]).all()
+    assert (~torch.isfinite(f.hs[bad_rows])).all(dim=1).all() and (~torch.isfinite(f.y[bad_rows])).all()
+    rest = bad_expert & ~bad_rows
+    assert rest.any() and torch.isnan(f.hs[rest][:, 1]).all() and torch.isnan(f.y[rest]).all()
+    assert torch.equal(f.hs[rest][:, [0, 2]], hs0[rest][:, [0, 2]])
