@@ -560,7 +560,9 @@ FT_API int ft_expert_ffn_decode_noalloc(const void* x, int T, int H, int I, int 
  *   y = r / sqrt(mean over H of r^2 + eps) * weight                   (f32)
  *   s = max(max |y| / 448, 2^-126) per 128 columns;  q = e4m3(y * (1 / s))
  * q is rounded to nearest even from the f32 y.  A NaN or infinity in y makes its block's
- * scale NaN or infinite (so every value of the block is NaN) and leaves the other rows alone.
+ * scale NaN or infinite (so every value of the block is NaN) and leaves the other rows alone.  The
+ * sum of squares is an f32: a row whose sum overflows (values from about 1e19) gets y = 0, one whose sum
+ * vanishes with eps = 0 (values below about 1e-23) infinities, and NaN for its zeros.
  *   x: [T][H], rows ldx elements apart, bf16 if x_is_bf16 else f32; residual (may be NULL) and
  *   residual_out (may be NULL; receives r): [T][H], rows ldr apart, x's type; residual_out may
  *   be residual, or x when ldx == ldr (refused when not, for T > 1); otherwise the buffers must not overlap.  weight: [H], x's
@@ -581,7 +583,7 @@ FT_API int ft_quantize_fp8(const void* x, long long ldx, int x_is_bf16, int T, i
  *   out[m][n] = sum over blocks b of K of a_scales[m][b] * w_scales[n / 128][b] *
  *               (sum over k in b of a[m][k] * w[n][k])
  * Tensor cores inside a block of 128, f32 sums across blocks.  The product of two scales that
- * meet has to be a finite f32.
+ * meet is formed first, as an f32: it has to be finite, and below 2^-126 it loses bits.
  *   a: [M][K] e4m3, rows lda bytes apart; a_scales: [M][ceil(K / 128)] f32 (as ft_rmsnorm_fp8 and
  *   ft_quantize_fp8 write them).  w: [N][K] e4m3, rows ldw bytes apart; w_scales:
  *   [ceil(N / 128)][ceil(K / 128)] f32.  out: [M][N], rows ldo elements apart, bf16 (round to

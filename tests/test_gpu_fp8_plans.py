@@ -235,6 +235,26 @@ def test_rmsnorm_many_wide_aligned_rows(T, H, bf16):
     check_codes(_bytes(q[:T, :H]), _np(s[:T]), ref, rel)
 
 
+@pytest.mark.parametrize("H", [512, 515])
+def test_norm_of_rows_whose_squares_leave_f32(H):
+    """As the header says: zeros where the sum of squares overflows, infinities and NaN where it vanishes and
+    eps is 0; the rows beside them are those of a call without such rows."""
+    x = torch.randn((6, H), device=DEV)
+    x[1], x[3], x[4] = 1e25, 1e-30, 0.0
+    x[3, 5] = 0.0
+    w = torch.full((H,), 0.5, device=DEV)
+    n = fp8.blocks(H)
+    y, q, s = torch.zeros_like(x), torch.zeros((6, H), dtype=torch.uint8, device=DEV), torch.zeros((6, n), device=DEV)
+    ft.ft_rmsnorm_fp8(x, H, None, 0, w, False, 6, H, 0.0, None, y, q, H, s)
+    assert (y[1] == 0).all() and (s[1] == fp8.TINY).all() and (q[1] == 0).all()
+    zero = x[3] == 0
+    assert torch.isnan(y[3][zero]).all() and torch.isinf(y[3][~zero]).all() and torch.isnan(y[4]).all()
+    keep = [0, 2, 5]
+    y2, q2, s2 = torch.zeros((3, H), device=DEV), torch.zeros((3, H), dtype=torch.uint8, device=DEV), torch.zeros((3, n), device=DEV)
+    ft.ft_rmsnorm_fp8(x[keep].contiguous(), H, None, 0, w, False, 3, H, 0.0, None, y2, q2, H, s2)
+    assert torch.equal(y[keep], y2) and torch.equal(q[keep], q2) and torch.equal(s[keep], s2)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("T,H", [(32, 7168), (300, 4096), (33, 2051), (5, 200)])
 def test_quantised_rows_are_the_formula_bit_for_bit(T, H, bf16):
