@@ -33,7 +33,7 @@ struct RowsFp8 {
   int T, H;
   float eps;
 };
-cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, cudaStream_t s);
+cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, int num_sms, cudaStream_t s);
 
 // Tensor maps of one product: A rows (128-byte boxes), and up to two weight matrices
 // [slots][rows][K] read 128 K bytes x 128 rows at a time.

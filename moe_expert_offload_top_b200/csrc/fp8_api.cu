@@ -1,5 +1,6 @@
 // C entry points of the fp8 operators (include/ftmoe.h): argument checks, tensor maps, launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <string>
 
@@ -22,10 +23,9 @@ int failed(const char* call, const char* what, cudaError_t e) {
 }
 bool aligned(const void* p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
-// The output must be memory of the current device: the launch would run there, and a host
-// address or another GPU's memory would fault it.
-int check_device(const char* call, const void* out) {
-  int dev = 0;
+// The output must be memory of the current device, which is returned in dev: the launch would run
+// there, and a host address or another GPU's memory would fault it.
+int check_device(const char* call, const void* out, int& dev) {
   cudaError_t e = cudaGetDevice(&dev);
   cudaPointerAttributes at{};
   if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, out);
@@ -38,10 +38,13 @@ int check_device(const char* call, const void* out) {
     return bad(call, "the output is not memory of the current device");
   return FT_OK;
 }
-int num_sms() {
-  int dev = 0, n = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+// SMs of a device; asked for once, as they do not change.
+int num_sms(int dev) {
+  static std::atomic<int> known[64];
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -111,9 +114,10 @@ int rows_call(const char* call, const ftk::RowsFp8& p, int x_is_bf16, void* stre
   if (!aligned(p.x, es) || !aligned(p.residual, es) || !aligned(p.weight, es) || !aligned(p.residual_out, es) ||
       !aligned(p.y, es) || !aligned(p.scales, 4))
     return bad(call, "a buffer is not aligned to its elements");
-  const int rc = check_device(call, p.q ? static_cast<const void*>(p.q) : p.y);
+  int dev = 0;
+  const int rc = check_device(call, p.q ? static_cast<const void*>(p.q) : p.y, dev);
   if (rc != FT_OK) return rc;
-  const cudaError_t e = ftk::launch_rows_fp8(p, x_is_bf16 != 0, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = ftk::launch_rows_fp8(p, x_is_bf16 != 0, num_sms(dev), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FT_OK : failed(call, "launch: ", e);
 }
 
@@ -132,9 +136,10 @@ int gemm_fp8(const char* call, const void* a, long long lda, const float* a_scal
   if (!aligned(a, 16) || !aligned(w, 16)) return bad(call, "a and w must be 16-byte aligned");
   if (!aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(out, out_is_bf16 ? 2 : 4) || !aligned(err, 4))
     return bad(call, "a buffer is not aligned to its elements");
-  const int rc = check_device(call, out);
+  int dev = 0;
+  const int rc = check_device(call, out, dev);
   if (rc != FT_OK) return rc;
-  const int sms = num_sms();
+  const int sms = num_sms(dev);
   const Plan pl =
       forced ? *forced : plan(1, M, 1, N, K, sms, ldo * (out_is_bf16 ? 2 : 4) % 16 == 0 && aligned(out, 16));
   ftk::Fp8Maps m;
@@ -188,12 +193,13 @@ int expert_ffn_fp8(const char* call, const void* x, long long ldx, const float* 
     groups.expert[i] = experts[i];
     groups.z[i] = slots[i];
   }
-  const int rc = check_device(call, y);
+  int dev = 0;
+  const int rc = check_device(call, y, dev);
   if (rc != FT_OK) return rc;
   const uint64_t pairs = (uint64_t)T * top_k + T, n = (uint64_t)H * I, blob = ft_fp8_blob_bytes(H, I);
   const size_t sb = 4 * (size_t)ftk::fp8_blocks(H) * ftk::fp8_blocks(I);
   const uint8_t* w = static_cast<const uint8_t*>(weights);
-  const int sms = num_sms();
+  const int sms = num_sms(dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* ws = w + 3 * n;
   const ftk::Fp8Gemm g{x_scales, {ws, ws + sb}, (long long)blob, offsets, perm, T, top_k, I, H, h, h_scales, I, 0, err,

@@ -5,8 +5,8 @@
 //   s = max(max |y| / 448, 2^-126)   per 128 columns of a row
 //   q = e4m3(y * (1 / s))            round to nearest even
 //
-// Bound by memory: one pass, each element read once into registers (8 per thread and chunk)
-// and written once per output; sums, norm and scales are fp32, and the only roundings to fewer
+// Bound by memory: one pass, each element read once into registers (16 per thread and chunk of
+// aligned rows, 8 of others) and written once per output; sums, norm and scales are fp32, and the only roundings to fewer
 // bits are the stored r, y and q (q from the fp32 y, not from the stored one).
 //
 // A row belongs to `tpr` threads (whole warps), so a row's sum is a warp sum plus one exchange
@@ -225,7 +225,7 @@ cudaError_t launch_rows(const RowsFp8& p, bool vec, int ch, dim3 grid, dim3 bloc
 
 }  // namespace
 
-cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, cudaStream_t s) {
+cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, int num_sms, cudaStream_t s) {
   if (p.T <= 0) return cudaSuccess;
   auto aligned = [](const void* q, int bytes) { return ((uintptr_t)q & (bytes - 1)) == 0; };
   const bool vec = p.H % 16 == 0 && p.ldx % 16 == 0 && aligned(p.x, 32) &&
@@ -236,7 +236,7 @@ cudaError_t launch_rows_fp8(const RowsFp8& p, bool x_bf16, cudaStream_t s) {
   // store.  Many wide rows with a norm, whose threads wait for one another, take two (8192 x 7168
   // bf16: 110 -> 96 us; without a norm one is better, 30 against 36).
   const int unit = 32 * elements(vec), units = (p.H + unit - 1) / unit;
-  const int most = vec && p.weight && p.T > 2 * 148 ? 8 : 32;
+  const int most = vec && p.weight && p.T > 2 * num_sms ? 8 : 32;
   int ch = 1;
   while (ch < (vec ? 2 : 4) && (units + ch - 1) / ch > most) ch *= 2;
   const int warps = (units + ch - 1) / ch;
