@@ -65,8 +65,10 @@ cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& maps, const GemmGroups& gro
 // The same product with the weights as the tensor cores' M, for few rows (fp8_stream.cu): nt
 // tokens (16, 32; mode 0: 64, mode 1: 128) per CTA, K split over clusters of `split` CTAs (1 .. 8, at most
 // the blocks of K), `chunks` CTAs sharing a group's token chunks.  maps.a: mode 0 boxes of one
-// row of x, mode 1 of nt rows.  after_gate_up: this launch directly follows the gate/up launch
-// (mode 0 of this kernel) that writes its rows, and loads weights while that one finishes.
+// row of x, mode 1 of nt rows.  after_gate_up: this launch may start, and load weights, while the launch
+// before it on the stream finishes, and waits for that one's end before it reads its rows.  The
+// launch before it must itself start behind the end of every launch that writes those rows or
+// offsets (no programmatic start of its own), as all gate/up launches do.
 cudaError_t launch_fp8_stream(int mode, int nt, int split, int chunks, const Fp8Maps& maps, const GemmGroups& groups,
                               const Fp8Gemm& p, bool after_gate_up, cudaStream_t s);
 // dst + q * stride = the H bytes of pair q's token row, for the pairs of the groups.

@@ -57,9 +57,12 @@ struct Plan {
 // takes a time of its own (more where K is split: the exchange of the sums) and a time per block of
 // K, less of it where two share an SM (`pair`); an SM runs its CTAs in turn.  The tiles take a
 // fixed time, and per wave a time per block and one for the stores.  No plan is faster than the
-// weights' bytes.  What it decides, measured: 4096 x 4096 weights, 1 row 7.8 against 18.7 on the
-// tiles, 200 rows 16.8 against 21.8, 384 rows 22.9 against 22.1; 100 x 512 x 512 with 16 tokens per
-// CTA and K in four 4.2, with 128 tokens 7.9.
+// weights' bytes.  It knows the average of a routing only: where one expert has most tokens, its
+// CTAs take them in turn while the others have left.  What it decides, measured (us, bf16 out):
+//   4096 x 4096 weights, 1 row: 16 tokens per CTA, K in four 6.7; tiles 18.0
+//   200 rows: 128 tokens, K in two 16.4; tiles 20.6.  384 rows: tiles 20.8; 128 tokens 22.4
+//   100 x 512 x 512: 16 tokens, K whole 4.7; K in four 4.5, 128 tokens 6.9, tiles 7.5
+//   gate/up with 64 tokens, FFN of 4096 x 128 x 128 one expert: 19.3; tiles 24.5 (4096 x 4096 x 128: 54 and 62)
 Plan plan(int mode, long long rows, int groups, int N, int K, int sms, bool aligned_rows) {
   struct Kind {
     int nt;

@@ -27,8 +27,9 @@
 //               loop must not spill: the reloads miss the small L1 beside the ring (8 bytes of
 //               spill cost 10 % of the kernel).
 //
-// What bounds it: 8192 x 7168 x 4096 takes 240 us, 2.0 PFLOP/s (cuBLAS reaches 3.3 at 8192^3 with one
-// scale per tensor, that is, without leaving TMEM).  The tensor cores alone would take 515 cycles
+// What bounds it: 8192 x 7168 x 4096 takes 240 to 244 us, 2.0 PFLOP/s, a hundred times in a row, and
+// 283 us, 1.7 PFLOP/s, over seconds, when the power cap lowers the clock (cuBLAS reaches 3.3 at 8192^3 in
+// short runs with one scale per tensor, that is, without leaving TMEM).  The tensor cores alone would take 515 cycles
 // per block of K (616 with the loads running); the loop takes about 850, because a TMEM buffer is
 // free only after release -> issue (200) -> its MMAs and commit (700 to 800) -> loads and
 // three quarters of the multiply-adds (600), and two buffers of 256 columns fill TMEM.  Tried and
@@ -461,11 +462,11 @@ fp8_gather_kernel(const uint8_t* x, long long ldx, const __grid_constant__ GemmG
     for (int i = lane; i < n; i += 128) {   // four loads in flight per lane
       uint4 v[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (i + 32 * x < n) v[x] = from[i + 32 * x];
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < n) v[j] = from[i + 32 * j];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (i + 32 * x < n) to[i + 32 * x] = v[x];
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < n) to[i + 32 * j] = v[j];
     }
   }
 }
