@@ -409,3 +409,69 @@ def test_ffn_keeps_nan_and_infinities_to_their_rows(form):
     rest = bad_expert & ~bad_rows
     assert rest.any() and torch.isnan(f.hs[rest][:, 1]).all() and torch.isnan(f.y[rest]).all()
     assert torch.equal(f.hs[rest][:, [0, 2]], hs0[rest][:, [0, 2]])
+
+
+# --------------------------- calls that the header allows, at odd addresses and lists --
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("plan", [TILES, (16, 2, 1), (128, 1, 2)])
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_gemm_into_rows_at_any_element(plan, bf16, off):
+    """out begins `off` elements behind a wide boundary while its rows are 32 bytes apart in step."""
+    M, N, K = 140, 272, 384
+    ld, a, w, sa, sw = _gemm_case(M, N, K, off)
+    flat, err = torch.full((M * N + 16,), 77.0, dtype=_dt(bf16), device=DEV), _err()
+    out = flat[off:off + M * N].view(M, N)
+    ft.ft_debug_gemm_fp8(a, ld, sa, w, ld, sw, M, N, K, bf16, out, N, err, plan)
+    assert err.item() == 0
+    _check_product(out, a, sa, w, sw, K, bf16)
+    assert (flat[:off] == 77).all() and (flat[off + M * N:] == 77).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("odd", ["x", "residual", "weight", "residual_out", "y", "q", "scales"])
+def test_norm_with_one_buffer_at_an_odd_element(odd, bf16):
+    T, H = 21, 640
+    g = torch.Generator().manual_seed(4)
+
+    def place(name, t):
+        off = 1 if name == odd else 0
+        flat = torch.zeros(t.numel() + 64, dtype=t.dtype, device=DEV)
+        view = flat[off:off + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+    x, res = (place(n, torch.randn((T, H), generator=g).to(_dt(bf16))) for n in ("x", "residual"))
+    w = place("weight", (1 + 0.3 * torch.randn(H, generator=g)).to(_dt(bf16)))
+    r, y = (place(n, torch.zeros((T, H), dtype=_dt(bf16))) for n in ("residual_out", "y"))
+    q, s = place("q", torch.zeros((T, H), dtype=torch.uint8)), place("scales", torch.zeros((T, 5)))
+    ft.ft_rmsnorm_fp8(x, H, res, H, w, bf16, T, H, EPS, r, y, q, H, s)
+    want = (x.float() + res.float()).to(_dt(bf16))
+    assert torch.equal(r, want)
+    ref = fp8.rmsnorm(_np(want), _np(w), EPS)
+    rel = _norm_bound(H)
+    assert (np.abs(_np(y) - ref) <= (rel + (UBF if bf16 else 0.0)) * np.abs(ref) * (1 + UBF) + 1e-38).all()
+    check_codes(_bytes(q), _np(s), ref, rel)
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_expert_ffn_of_the_shared_expert_alone(T):
+    f = Ffn(T, 272, 400, 4, 2, True, seed=6)
+    f.run(experts=[-1], slots=[f.slots[f.experts.index(-1)]])
+    f.check(skip=range(4))
+
+
+@pytest.mark.parametrize("T", [1, 60])
+def test_expert_ffn_with_the_list_turned_round(T):
+    """The list's order does not matter: the shared expert first, the others from the last."""
+    f = Ffn(T, 256, 144, 16, 3, True, seed=7, empty=(2,))
+    f.run(experts=f.experts[::-1], slots=f.slots[::-1])
+    f.check()
+
+
+@pytest.mark.parametrize("T,forced", [(1, None), (9, None), (70, None), (70, TILES)])
+def test_expert_ffn_with_every_expert_listed(T, forced):
+    """256 routed experts and the shared one, most of them without tokens: what a captured call lists."""
+    f = PlannedFfn(T, 144, 80, 256, 6, True, seed=12) if forced else Ffn(T, 144, 80, 256, 6, True, seed=12)
+    assert len(f.experts) == 257
+    f.run()
+    f.check()
